@@ -336,6 +336,145 @@ size_t arx_max_n(void);
 int arx_world(void);
 int arx_rank(void);
 
+/*
+ * ---- layer operators ------------------------------------------------------
+ *
+ * What stands on either side of the all-reduce of a tensor-parallel layer:
+ * the product whose rows a rank sums into its partial (arx_linear), and the
+ * join of the summed partial with bias, dropout, residual and layer norm
+ * (arx_dropout_add, arx_layer_norm, arx_dropout_add_norm), each with its
+ * backward pass. They need no arx_init, keep nothing between calls, allocate
+ * nothing and may be captured in a hipGraph; calls on different streams do
+ * not disturb each other.
+ *
+ * Conventions, beside those above:
+ *   - dtype: ARX_BF16, ARX_F16 or ARX_F32 (the linear calls: the first two);
+ *     wdtype, the type of a norm's weight and shift: dtype or ARX_F32.
+ *   - a plane of rows is a pointer and a row distance ld >= cols in elements:
+ *     element (r, c) at p[r * ld + c]. Any element-aligned address and any
+ *     ld will do; a vector (bias, weight, shift, mean, ...) is contiguous.
+ *   - sizes are 0 .. 2^31 - 1 each. Nothing is launched where every output is
+ *     empty; a sum over no rows is written as zero.
+ *   - sums, means and variances are binary32; each output is rounded once,
+ *     to nearest, ties to even.
+ *   - an output may take an input plane's place (same address, same ld) where
+ *     the call says so; any other overlap of an output with anything else is
+ *     ARX_EINVAL.
+ *   - sums run in a fixed order: the same call gives the same bits.
+ * Errors of all of them (nothing launched): ARX_EINVAL, ARX_EHIP.
+ */
+#define ARX_BF16 0
+#define ARX_F16 1
+#define ARX_F32 2
+
+#define ARX_ACT_NONE 0
+#define ARX_ACT_RELU 1      /* z where z > 0, else 0; NaN stays */
+#define ARX_ACT_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define ARX_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define ARX_ACT_SILU 4      /* z / (1 + e^-z) */
+
+/*
+ * arx_linear — y = act(z) + residual, z = x w^T + bias: x [m][k], w [n][k],
+ * bias [n] or NULL, residual [m][n] or NULL, y [m][n], z [m][n] or NULL (kept
+ * for arx_linear_backward). y may take residual's place.
+ *   workspace: 16-byte aligned device memory of at least
+ *   arx_linear_workspace(m, n, k, dtype) bytes (0: may be NULL), used by this
+ *   call alone until it has run.
+ */
+int arx_linear(const void* x, const void* w, const void* bias, const void* residual, void* y, void* z, size_t m,
+               size_t n, size_t k, size_t ldx, size_t ldw, size_t ldr, size_t ldy, size_t ldz, int act, int dtype,
+               void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t arx_linear_workspace(size_t m, size_t n, size_t k, int dtype);
+
+/*
+ * arx_linear_backward — with g = dy act'(z): dx [m][k] = g w, dw [n][k] =
+ * g^T x, dbias [n] = sum over rows of g (dresidual is dy). Any of dx, dw and
+ * dbias may be NULL; x is read for dw, w for dx, z unless act is
+ * ARX_ACT_NONE, and those that are not read may be NULL. g enters the
+ * products rounded to dtype, and dbias as it is.
+ *   workspace: as for arx_linear, arx_linear_backward_workspace(...) bytes.
+ */
+int arx_linear_backward(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw, void* dbias,
+                        size_t m, size_t n, size_t k, size_t lddy, size_t ldx, size_t ldw, size_t ldz, size_t lddx,
+                        size_t lddw, int act, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int dtype);
+
+/*
+ * arx_layer_norm — over each row of x [rows][cols]: y = (x - mean) rstd
+ * weight + shift, rstd = 1 / sqrt(variance + eps), the variance divided by
+ * cols. weight, shift [cols] or NULL (1 and 0); mean, rstd: f32 [rows] out,
+ * or NULL. y may take x's place. eps >= 0.
+ */
+int arx_layer_norm(const void* x, const void* weight, const void* shift, void* y, float* mean, float* rstd,
+                   size_t rows, size_t cols, size_t ldx, size_t ldy, double eps, int dtype, int wdtype,
+                   hipStream_t stream);
+
+/*
+ * arx_layer_norm_backward — dx [rows][cols], and with xh = (x - mean) rstd:
+ * dweight [cols] = sum over rows of dy xh, dshift [cols] = sum of dy (each
+ * wdtype, or NULL). dx may take dy's or x's place.
+ *   workspace: 16-byte aligned, arx_rows_workspace(rows, cols, 2) bytes.
+ */
+int arx_layer_norm_backward(const void* dy, const void* x, const float* mean, const float* rstd, const void* weight,
+                            void* dx, void* dweight, void* dshift, size_t rows, size_t cols, size_t lddy, size_t ldx,
+                            size_t lddx, int dtype, int wdtype, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * arx_dropout_add — h = residual + keep ? s (x + bias) : 0, each [rows][cols];
+ * bias [cols] or NULL, residual or NULL. The mask is never stored: element
+ * (r, c) is kept if u(r, c) >= T, where u is 16 bits of a counter-based
+ * generator, Philox4x32 with 10 rounds, key seed, counter words
+ * (r * ceil(cols / 8) + c / 8, offset), 64 bits each, low word first: half
+ * c % 8 of its four output words, the low half of a word first. T is 65536 p
+ * rounded to nearest, ties to even, s = 65536 / (65536 - T), so a kept
+ * element's expectation is exact; 0 <= p <= 1, and p = 1 drops everything.
+ * The same seed and offset give the same mask on every rank; another layer or
+ * step takes another offset. h may take x's or residual's place.
+ */
+int arx_dropout_add(const void* x, const void* bias, const void* residual, void* h, size_t rows, size_t cols,
+                    size_t ldx, size_t ldr, size_t ldh, double p, uint64_t seed, uint64_t offset, int dtype,
+                    hipStream_t stream);
+
+/*
+ * arx_dropout_add_backward — dx = keep ? s dh : 0 with the mask of the forward
+ * call (same rows, cols, p, seed, offset), dbias [cols] or NULL = sum over
+ * rows of dx (dresidual is dh). dx may be NULL, or take dh's place.
+ *   workspace: 16-byte aligned, arx_rows_workspace(rows, cols, 1) bytes; not
+ *   needed without dbias.
+ */
+int arx_dropout_add_backward(const void* dh, void* dx, void* dbias, size_t rows, size_t cols, size_t lddh, size_t lddx,
+                             double p, uint64_t seed, uint64_t offset, int dtype, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * arx_dropout_add_norm — h as in arx_dropout_add and y, mean, rstd the layer
+ * norm of h, in one pass. The norm takes h before it is rounded. h may be
+ * NULL (not wanted). h and y may each take x's or residual's place.
+ */
+int arx_dropout_add_norm(const void* x, const void* bias, const void* residual, const void* weight,
+                         const void* shift, void* h, void* y, float* mean, float* rstd, size_t rows, size_t cols,
+                         size_t ldx, size_t ldr, size_t ldh, size_t ldy, double eps, double p, uint64_t seed,
+                         uint64_t offset, int dtype, int wdtype, hipStream_t stream);
+
+/*
+ * arx_dropout_add_norm_backward — dy the gradient of y, dh that of h from its
+ * other users (or NULL): dresidual = norm backward of dy + dh, dx = dresidual
+ * before its rounding, dropped as in the forward call, dbias = sum over rows
+ * of dx (as dtype), dweight and dshift (as wdtype). dresidual, dbias, dweight
+ * and dshift may be NULL. dx and dresidual may each take dy's, dh's or h's
+ * place.
+ *   workspace: 16-byte aligned, arx_rows_workspace(rows, cols, 3) bytes.
+ */
+int arx_dropout_add_norm_backward(const void* dy, const void* dh, const void* h, const float* mean, const float* rstd,
+                                  const void* weight, void* dx, void* dresidual, void* dbias, void* dweight,
+                                  void* dshift, size_t rows, size_t cols, size_t lddy, size_t lddh, size_t ldh,
+                                  size_t lddx, size_t lddr, double p, uint64_t seed, uint64_t offset, int dtype,
+                                  int wdtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for `sums` (1..3) column sums over rows x cols. */
+size_t arx_rows_workspace(size_t rows, size_t cols, int sums);
+
 #ifdef __cplusplus
 }
 #endif

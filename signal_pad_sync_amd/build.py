@@ -7,12 +7,15 @@ harmless.
 """
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libarx.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("arx_reduce.hip", "arx_sync.hip", "arx_runtime.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("arx_reduce.hip", "arx_sync.hip", "arx_rows.hip", "arx_linear.hip",
+                                            "arx_runtime.cpp", "arx_layer.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -25,10 +28,18 @@ FLAGS = [
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    cmd = [HIPCC, *FLAGS, *extra, *SOURCES, "-o", LIB + ".tmp", "-lpthread"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    """Compiles the sources side by side, then links."""
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        commands = [[HIPCC, *flags, *extra, "-c", src, "-o", obj] for src, obj in zip(SOURCES, objects)]
+        link = [HIPCC, "--offload-arch=gfx950", "-shared", *extra, *objects, "-o", LIB + ".tmp", "-lpthread"]
+        if verbose:
+            for cmd in (*commands, link):
+                print(" ".join(cmd), flush=True)
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda cmd: subprocess.run(cmd, check=True), commands))
+        subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 
