@@ -378,13 +378,15 @@ int arx_rank(void);
  * bias [n] or NULL, residual [m][n] or NULL, y [m][n], z [m][n] or NULL (kept
  * for arx_linear_backward). y may take residual's place.
  *   workspace: 16-byte aligned device memory of at least
- *   arx_linear_workspace(m, n, k, dtype) bytes (0: may be NULL), used by this
- *   call alone until it has run.
+ *   arx_linear_workspace(m, n, k, aligned) bytes (0: may be NULL), used by
+ *   this call alone until it has run. aligned: 1 if x and w start on 16-byte
+ *   boundaries and their row distances are multiples of 8 below 2^22, else 0
+ *   (rows off those boundaries are copied onto them first).
  */
 int arx_linear(const void* x, const void* w, const void* bias, const void* residual, void* y, void* z, size_t m,
                size_t n, size_t k, size_t ldx, size_t ldw, size_t ldr, size_t ldy, size_t ldz, int act, int dtype,
                void* workspace, size_t workspace_bytes, hipStream_t stream);
-size_t arx_linear_workspace(size_t m, size_t n, size_t k, int dtype);
+size_t arx_linear_workspace(size_t m, size_t n, size_t k, int aligned);
 
 /*
  * arx_linear_backward — with g = dy act'(z): dx [m][k] = g w, dw [n][k] =
@@ -392,12 +394,13 @@ size_t arx_linear_workspace(size_t m, size_t n, size_t k, int dtype);
  * dbias may be NULL; x is read for dw, w for dx, z unless act is
  * ARX_ACT_NONE, and those that are not read may be NULL. g enters the
  * products rounded to dtype, and dbias as it is.
- *   workspace: as for arx_linear, arx_linear_backward_workspace(...) bytes.
+ *   workspace: as for arx_linear, arx_linear_backward_workspace(...) bytes;
+ *   aligned: of dy, x and w.
  */
 int arx_linear_backward(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw, void* dbias,
                         size_t m, size_t n, size_t k, size_t lddy, size_t ldx, size_t ldw, size_t ldz, size_t lddx,
                         size_t lddw, int act, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
-size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int dtype);
+size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int aligned);
 
 /*
  * arx_layer_norm — over each row of x [rows][cols]: y = (x - mean) rstd

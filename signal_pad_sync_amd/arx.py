@@ -430,6 +430,11 @@ def _act(act):
     return ACTS[act]
 
 
+def _on_lines(p, ld):
+    """Rows that all start on 16-byte boundaries (arx.h, arx_linear)."""
+    return not p & 15 and not ld & 7 and ld < 1 << 22
+
+
 def linear(x, w, bias=None, residual=None, act="none", save_z=False, out=None, stream=None):
     """y = act(z) + residual with z = x w^T + bias; x [m, k], w [n, k], bias
     [n], residual [m, n], all bf16 or all f16. Returns y, or (y, z) with
@@ -448,7 +453,7 @@ def linear(x, w, bias=None, residual=None, act="none", save_z=False, out=None, s
         out = c.empty(m, n)
     yp, ldy = c.plane(out, "out", (m, n))
     z = c.empty(m, n) if save_z else None
-    space = lib.arx_linear_workspace(m, n, k, c.code)
+    space = lib.arx_linear_workspace(m, n, k, _on_lines(xp, ldx) and _on_lines(wp, ldw))
     hold, space_p = c.workspace(space)
     _check(lib.arx_linear(xp, wp, c.vector(bias, "bias", n), rp, yp, z.data_ptr() if save_z else None, m, n, k, ldx,
                           ldw, ldr, ldy, n, kind, c.code, space_p, space, c.stream))
@@ -473,7 +478,8 @@ def linear_backward(dy, x, w, z=None, act="none", dx=True, dw=True, dbias=False,
     gx = c.empty(m, k) if dx else None
     gw = c.empty(n, k) if dw else None
     gb = c.empty(n) if dbias else None
-    space = lib.arx_linear_backward_workspace(m, n, k, kind, c.code)
+    space = lib.arx_linear_backward_workspace(
+        m, n, k, kind, _on_lines(dyp, lddy) and _on_lines(xp, ldx) and _on_lines(wp, ldw))
     hold, space_p = c.workspace(space)
     _check(lib.arx_linear_backward(dyp, xp, wp, zp, _ptr(gx), _ptr(gw), _ptr(gb), m, n, k, lddy, ldx, ldw, ldz, k, k,
                                    kind, c.code, space_p, space, c.stream))

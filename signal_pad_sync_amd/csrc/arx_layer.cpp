@@ -136,15 +136,19 @@ struct LinearSpace {
   size_t g = 0, rest = 0;
   size_t total() const { return g + rest; }
 };
-LinearSpace linear_space(size_t m, size_t n, size_t k, int act, int dtype) {
+LinearSpace linear_space(size_t m, size_t n, size_t k, int act, bool aligned) {
   LinearSpace s;
-  if (act != ARX_ACT_NONE) s.g = round_up(m * n * size_of(dtype));
+  if (act != ARX_ACT_NONE) s.g = round_up(m * ((n + 7) & ~(size_t)7) * 2);
   const size_t parts[3] = {arx::act_grad_workspace(m, n),
-                           arx::gemm_workspace((uint32_t)m, (uint32_t)k, (uint32_t)n, false, true),
-                           arx::gemm_workspace((uint32_t)n, (uint32_t)k, (uint32_t)m, true, true)};
+                           arx::gemm_workspace((uint32_t)m, (uint32_t)k, (uint32_t)n, false, true, aligned),
+                           arx::gemm_workspace((uint32_t)n, (uint32_t)k, (uint32_t)m, true, true, aligned)};
   for (size_t b : parts) s.rest = b > s.rest ? b : s.rest;
   return s;
 }
+
+// Whether a plane's rows all start on 16-byte boundaries, near enough for a
+// tile's 32-bit offsets.
+bool on_lines(const void* p, size_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && ld < ((size_t)1 << 22); }
 
 int check_linear(size_t m, size_t n, size_t k, int act, int dtype) {
   TRY(check_sizes(m, n, k));
@@ -157,10 +161,9 @@ int check_linear(size_t m, size_t n, size_t k, int act, int dtype) {
 
 extern "C" {
 
-size_t arx_linear_workspace(size_t m, size_t n, size_t k, int dtype) {
-  (void)dtype;
+size_t arx_linear_workspace(size_t m, size_t n, size_t k, int aligned) {
   if (m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
-  return arx::gemm_workspace((uint32_t)m, (uint32_t)n, (uint32_t)k, false, false);
+  return arx::gemm_workspace((uint32_t)m, (uint32_t)n, (uint32_t)k, false, false, aligned != 0);
 }
 
 int arx_linear(const void* x, const void* w, const void* bias, const void* residual, void* y, void* z, size_t m,
@@ -173,7 +176,8 @@ int arx_linear(const void* x, const void* w, const void* bias, const void* resid
   TRY(need("y", y));
   TRY(check({in("x", x, m, k, ldx, 2), in("w", w, n, k, ldw, 2), in("bias", bias, 1, n, n, 2),
              in("residual", residual, m, n, ldr, 2, true), out("y", y, m, n, ldy, 2), out("z", z, m, n, ldz, 2)}));
-  TRY(check_workspace(workspace, workspace_bytes, arx_linear_workspace(m, n, k, dtype)));
+  TRY(check_workspace(workspace, workspace_bytes,
+                      arx_linear_workspace(m, n, k, on_lines(x, ldx) && on_lines(w, ldw))));
   arx::GemmArgs g{};
   g.a = x;
   g.b = w;
@@ -191,9 +195,9 @@ int arx_linear(const void* x, const void* w, const void* bias, const void* resid
   return launched(arx::launch_gemm(g, dtype, stream), "arx_linear");
 }
 
-size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int dtype) {
+size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int aligned) {
   if (m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
-  return linear_space(m, n, k, act, dtype).total();
+  return linear_space(m, n, k, act, aligned != 0).total();
 }
 
 int arx_linear_backward(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw, void* dbias,
@@ -213,7 +217,7 @@ int arx_linear_backward(const void* dy, const void* x, const void* w, const void
   TRY(check({in("dy", dy, m, n, lddy, 2), in("x", dw ? x : nullptr, m, k, ldx, 2),
              in("w", dx ? w : nullptr, n, k, ldw, 2), in("z", z, m, n, ldz, 2), out("dx", dx, m, k, lddx, 2),
              out("dw", dw, n, k, lddw, 2), out("dbias", dbias, 1, n, n, 2)}));
-  const LinearSpace s = linear_space(m, n, k, act, dtype);
+  const LinearSpace s = linear_space(m, n, k, act, on_lines(dy, lddy) && on_lines(x, ldx) && on_lines(w, ldw));
   TRY(check_workspace(workspace, workspace_bytes, s.total()));
   char* const rest = static_cast<char*>(workspace) + s.g;
 
@@ -231,7 +235,8 @@ int arx_linear_backward(const void* dy, const void* x, const void* w, const void
   }
   arx::GemmArgs g{};
   g.a = slope ? workspace : dy;
-  g.lda = (int64_t)(slope ? n : lddy);
+  g.lda = (int64_t)(slope ? (n + 7) & ~(size_t)7 : lddy);
+  g.a_whole = slope;
   g.act = ARX_ACT_NONE;
   g.workspace = rest;
   if (dx) {

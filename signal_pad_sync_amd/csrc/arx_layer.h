@@ -62,8 +62,9 @@ hipError_t launch_norm_backward(const RowsGradArgs& a, bool join, int dtype, int
 // Bytes of workspace the backward launchers need for `sums` column sums.
 size_t rows_workspace(size_t rows, size_t cols, int sums);
 
-// g = dy * act'(z) into `g` (contiguous [m][n]) and its column sums into dbias;
-// either may be null. act none: dbias alone.
+// g = dy * act'(z) into `g` ([m][n] rounded up to a multiple of eight columns,
+// the last ones zero) and its column sums into dbias; either may be null. act
+// none: dbias alone.
 struct ActGradArgs {
   Plane dy, z;
   void* g;
@@ -81,15 +82,17 @@ struct GemmArgs {
   const void *a, *b;
   int64_t lda, ldb;
   bool a_rows_k, b_rows_k;
+  bool a_whole;  // a's lines go on to a multiple of eight elements, in zeros
   uint32_t m, n, k;
   const void* bias;
   Plane residual;
   PlaneOut y, z;
   int act;
   void* workspace;
-  size_t workspace_bytes;
 };
 hipError_t launch_gemm(const GemmArgs& a, int dtype, hipStream_t stream);
-size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k);
+// aligned: both operands start on 16-byte boundaries and their ld is a
+// multiple of 8 below 2^22.
+size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned);
 
 }  // namespace arx

@@ -1,7 +1,9 @@
 // arx_linear.hip — matrix products for gfx950 with bias, activation and
 // residual in the epilogue.
 //
-//   gemm_kernel   C = A B^T on the matrix cores, 128 x 128 tiles
+//   tile_kernel   C = A B^T on the matrix cores, tile by tile
+//   join_kernel   adds the splits of a long depth, in order
+//   pad_kernel    rows that start off 16-byte boundaries, copied onto them
 //
 // Sums are binary32 in the matrix cores' accumulators; z and y are each
 // rounded once, from the same binary32 value.
@@ -15,11 +17,11 @@ namespace {
 
 __host__ __device__ constexpr uint32_t cdiv(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ float act_any(int kind, float z) {
@@ -32,114 +34,386 @@ __device__ __forceinline__ float act_any(int kind, float z) {
   }
 }
 
+// Eight sums of row i, columns j.. : bias, z, activation, residual, y.
 template <typename T>
-__device__ __forceinline__ f32x4 load4(const T* p, int valid) {
-  typename Vec<T>::x4 v;
-  if (valid >= 4) {
-    __builtin_memcpy(&v, p, sizeof v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < valid ? p[j] : (T)0.0f;
-  }
-  return __builtin_convertvector(v, f32x4);
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, f32x4 f, int valid) {
-  const typename Vec<T>::x4 v = __builtin_convertvector(f, typename Vec<T>::x4);
-  if (valid >= 4) {
-    __builtin_memcpy(p, &v, sizeof v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < valid) p[j] = v[j];
-  }
-}
-
-// Four sums of row i, columns j.. : bias, z, activation, residual, y.
-template <typename T>
-__device__ __forceinline__ void epilogue4(const GemmArgs& g, uint32_t i, uint32_t j, f32x4 c) {
+__device__ __forceinline__ void epilogue8(const GemmArgs& g, uint32_t i, uint32_t j, f32x8 c) {
   if (i >= g.m || j >= g.n) return;
-  const int valid = g.n - j < 4u ? (int)(g.n - j) : 4;
-  if (g.bias) c += load4(static_cast<const T*>(g.bias) + j, valid);
-  if (g.z.p) store4<T>(static_cast<T*>(g.z.p) + (int64_t)i * g.z.ld + j, c, valid);
+  const int valid = g.n - j < 8u ? (int)(g.n - j) : 8;
+  if (g.bias) c += widen(load8(static_cast<const T*>(g.bias) + j, valid));
+  if (g.z.p) store8<T>(static_cast<T*>(g.z.p) + (int64_t)i * g.z.ld + j, narrow<T>(c), valid);
   if (g.act != ARX_ACT_NONE) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = act_any(g.act, c[e]);
+    for (int e = 0; e < 8; ++e) c[e] = act_any(g.act, c[e]);
   }
-  if (g.residual.p) c += load4(static_cast<const T*>(g.residual.p) + (int64_t)i * g.residual.ld + j, valid);
-  store4<T>(static_cast<T*>(g.y.p) + (int64_t)i * g.y.ld + j, c, valid);
+  if (g.residual.p) c += widen(load8(static_cast<const T*>(g.residual.p) + (int64_t)i * g.residual.ld + j, valid));
+  store8<T>(static_cast<T*>(g.y.p) + (int64_t)i * g.y.ld + j, narrow<T>(c), valid);
 }
 
-// One operand's 128 x 32 tile: rows [r0, r0 + 128) of `rows`, k [k0, k0 + 32)
-// of `k`, elements past either end zero. ROWS_K: the row index is the
-// contiguous one, and the tile is turned on its way into shared memory.
-constexpr int kTile = 128, kDepth = 32, kPitch = kDepth + 8;
+// ---- tiles ------------------------------------------------------------------
 
-template <typename T, bool ROWS_K>
-__device__ __forceinline__ void stage(T* lds, const T* p, int64_t ld, uint32_t r0, uint32_t rows, uint32_t k0,
-                                      uint32_t k) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t t = threadIdx.x + i * 256u;
-    if constexpr (!ROWS_K) {
-      const uint32_t r = t / 4u, c = (t % 4u) * 8u;
-      const int valid = r0 + r < rows && k0 + c < k ? (int)min(8u, k - k0 - c) : 0;
-      *reinterpret_cast<typename Vec<T>::x8*>(lds + r * kPitch + c) =
-          load8(p + (int64_t)(r0 + r) * ld + (k0 + c), valid);
+// Operand tiles are kDepth = 64 deep and come to shared memory without passing
+// through registers, 16 bytes a lane. Two layouts, each with its 16-byte
+// chunks permuted so that the fragment reads meet no bank twice:
+//   depth-contiguous operand (row r, k contiguous): row r is 128 bytes, chunk
+//   c of it at place c ^ (r & 7);
+//   row-contiguous operand (ROWS_K): depth k is a line of TILE rows, 32-byte
+//   piece p of it at place p ^ (k & 3), read with the transposing LDS load.
+constexpr int kDepth = 64;
+
+// Sixteen zero bytes that lanes past the end of the depth read instead.
+__device__ const uint4 kZeros = {0, 0, 0, 0};
+
+typedef const __attribute__((address_space(1))) void* GlobalPtr;
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// One lane's 16 bytes from p to the wave's 1 KiB block at LDS offset `block`.
+__device__ __forceinline__ void to_lds(const void* p, char* block) {
+  __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)block, 16, 0, 0);
+}
+
+// What a wave loads of one operand's tile: block q * 4 + wave of 1 KiB.
+template <typename T, int TILE, bool ROWS_K>
+struct Loader {
+  static constexpr int BLOCKS = TILE / 32;   // per wave
+  static constexpr int LINES = ROWS_K ? 512 / TILE : 8;   // lines of a block: depths or rows
+  uint32_t off[ROWS_K ? 1 : BLOCKS];         // byte offset of this lane's chunk
+  uint32_t line;                             // first depth (ROWS_K) or first chunk of this lane
+  const char* base;                          // tile's corner, at depth 0
+  int64_t step;                              // bytes between depths (ROWS_K)
+
+  __device__ __forceinline__ void init(const void* p, int64_t ld, uint32_t r0, uint32_t rows, uint32_t wave) {
+    const uint32_t lane = threadIdx.x & 63u;
+    if constexpr (ROWS_K) {
+      constexpr uint32_t CHUNKS = TILE / 8;
+      line = wave * LINES + lane / CHUNKS;
+      uint32_t c = (lane % CHUNKS) ^ (2u * (line & 3u));
+      const uint32_t last = (rows - r0 - 1u) / 8u;    // a line holds its last chunk whole
+      if (c > last) c = last;                         // past it: a chunk again, for rows that nothing stores
+      off[0] = (uint32_t)(line * ld * sizeof(T)) + c * 16u;
+      base = reinterpret_cast<const char*>(static_cast<const T*>(p) + r0);
+      step = ld * sizeof(T);
     } else {
-      const uint32_t c = t / 16u, r = (t % 16u) * 8u;
-      const int valid = k0 + c < k && r0 + r < rows ? (int)min(8u, rows - r0 - r) : 0;
-      const typename Vec<T>::x8 v = load8(p + (int64_t)(k0 + c) * ld + (r0 + r), valid);
+      line = (lane & 7u) ^ (lane >> 3);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) lds[(r + j) * kPitch + c] = v[j];
+      for (int q = 0; q < BLOCKS; ++q) {
+        uint32_t r = (q * 4 + wave) * 8u + (lane >> 3);
+        if (r >= rows - r0) r = rows - r0 - 1u;
+        off[q] = (uint32_t)(r * ld * sizeof(T)) + line * 16u;
+      }
+      base = reinterpret_cast<const char*>(static_cast<const T*>(p) + (int64_t)r0 * ld);
+      step = sizeof(T);
     }
+  }
+
+  // Depths [k0, k0 + 64) into `lds`; those from k on are zero.
+  __device__ __forceinline__ void load(char* lds, uint32_t k0, uint32_t k, uint32_t wave) const {
+    const char* const at = base + (int64_t)k0 * step;
+    if (k0 + kDepth <= k) {
+#pragma unroll
+      for (int q = 0; q < BLOCKS; ++q) {
+        if constexpr (ROWS_K) to_lds(at + (int64_t)(q * 4 * LINES) * step + off[0], lds + (q * 4 + wave) * 1024u);
+        else to_lds(at + off[q], lds + (q * 4 + wave) * 1024u);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < BLOCKS; ++q) {
+        const char* src;
+        if constexpr (ROWS_K)
+          src = k0 + q * 4 * LINES + line < k ? at + (int64_t)(q * 4 * LINES) * step + off[0] : nullptr;
+        else
+          src = k0 + line * 8u < k ? at + off[q] : nullptr;
+        to_lds(src ? src : reinterpret_cast<const char*>(&kZeros), lds + (q * 4 + wave) * 1024u);
+      }
+    }
+  }
+};
+
+// A fragment for the 32 x 32 x 16 matrix instruction: lane l holds row l % 32,
+// depths 8 (l / 32) + 0..7 of the kk-th sixteen.
+template <typename T, int TILE, bool ROWS_K>
+struct Fragments {
+  typedef typename Vec<T>::x8 x8;
+  uint32_t at[ROWS_K ? 2 : 4];
+  // r0: the wave's first row, a multiple of 32, and of 64 where it has more than 32.
+  __device__ __forceinline__ void init(uint32_t r0) {
+    const uint32_t l = threadIdx.x & 63u;
+    if constexpr (ROWS_K) {
+      // A group of 16 lanes reads four depths of one 32-byte piece, 8 bytes a
+      // lane, and gets each row's four depths.
+      const uint32_t j = l & 15u, depth = (l >> 5) * 8u + (j >> 2), piece = (l >> 4) & 1u;
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+        at[p] = depth * (TILE * 2u) + r0 / 64u * 128u + (((r0 / 16u + 2u * p + piece) & 3u) ^ (j >> 2)) * 32u +
+                (j & 3u) * 8u;
+    } else {
+#pragma unroll
+      for (uint32_t kk = 0; kk < 4; ++kk) at[kk] = (r0 + (l & 31u)) * 128u + (((kk * 2u + (l >> 5)) ^ (l & 7u)) << 4);
+    }
+  }
+  // The wave's rows [32 x, 32 x + 32), the kk-th sixteen depths.
+  __device__ __forceinline__ x8 read(const char* lds, int x, int kk) const {
+    if constexpr (ROWS_K) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4* P;
+      const char* const p = lds + at[x & 1] + (x >> 1) * 128 + kk * (16 * TILE * 2);
+      union {
+        s16x4 half[2];
+        x8 all;
+      } u;
+      u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+      u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 4 * TILE * 2));
+      return u.all;
+    } else {
+      return *reinterpret_cast<const x8*>(lds + at[kk] + x * 4096);
+    }
+  }
+};
+
+// Waits until at most N of the wave's loads are outstanding and its LDS reads
+// are done, then meets the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+struct TileArgs {
+  GemmArgs g;
+  uint32_t tiles_n, tiles;  // tiles across, in all
+  uint32_t depth;           // k of one split, a multiple of kDepth
+  float* partial;           // [splits][m][n], or null: one split, with the epilogue
+};
+
+// Workgroup -> tile. Workgroups go round the 8 XCDs, each with an L2 of its
+// own: an XCD takes consecutive tiles, and tiles run down 8 rows before the
+// next column, so that what an XCD works on at a time shares operands.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t tiles_n, uint32_t* ti, uint32_t* tj) {
+  const uint32_t xcd = id & 7u, each = tiles >> 3, more = tiles & 7u;
+  const uint32_t t = xcd * each + (xcd < more ? xcd : more) + (id >> 3);
+  const uint32_t band = 8u * tiles_n, first = t / band * 8u, tiles_m = tiles / tiles_n;
+  const uint32_t high = tiles_m - first < 8u ? tiles_m - first : 8u, in = t % band;
+  *ti = first + in % high;
+  *tj = in / high;
+}
+
+// C's TM x TN tile on four waves, each (TM / 2) x (TN / 2) in 32 x 32 blocks.
+// The depth runs through NS buffers: while the matrix cores work on one, the
+// loads of the next NS - 1 are under way. B's fragments take the matrix
+// instruction's rows, so a lane's sums are neighbours in a row of C.
+template <typename T, int TM, int TN, int NS, bool A_ROWS_K, bool B_ROWS_K>
+__global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
+  constexpr int MI = TM / 64, NI = TN / 64, BYTES = (TM + TN) * 128;
+  constexpr int LOADS = TM / 32 + TN / 32, PITCH = TN / 2 + 4;
+  static_assert(4 * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
+  static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
+  __shared__ __align__(1024) char lds[NS * BYTES];
+  const GemmArgs& g = t.g;
+  uint32_t ti, tj;
+  tile_of(blockIdx.x, t.tiles, t.tiles_n, &ti, &tj);
+  const uint32_t i0 = ti * TM, j0 = tj * TN, lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = (wave >> 1) * (TM / 2),
+                 wj = (wave & 1u) * (TN / 2);
+  const uint32_t k_first = blockIdx.y * t.depth, k_last = min(g.k, k_first + t.depth);
+  const uint32_t steps = k_last > k_first ? (k_last - k_first + kDepth - 1) / kDepth : 0u;
+  Loader<T, TM, A_ROWS_K> la;
+  Loader<T, TN, B_ROWS_K> lb;
+  la.init(g.a, g.lda, i0, g.m, wave);
+  lb.init(g.b, g.ldb, j0, g.n, wave);
+  Fragments<T, TM, A_ROWS_K> ra;
+  Fragments<T, TN, B_ROWS_K> rb;
+  ra.init(wi);
+  rb.init(wj);
+  f32x16 c[MI][NI];
+#pragma unroll
+  for (int x = 0; x < MI; ++x)
+#pragma unroll
+    for (int y = 0; y < NI; ++y) c[x][y] = f32x16(0.0f);
+  typename Vec<T>::x8 fa[2][MI], fb[2][NI];
+
+  const auto load = [&](uint32_t s) {
+    char* const buf = lds + (s % NS) * BYTES;
+    la.load(buf, k_first + s * kDepth, k_last, wave);
+    lb.load(buf + TM * 128, k_first + s * kDepth, k_last, wave);
+  };
+  const auto read = [&](uint32_t s, int kk, int to) {
+    const char* const buf = lds + (s % NS) * BYTES;
+#pragma unroll
+    for (int x = 0; x < MI; ++x) fa[to][x] = ra.read(buf, x, kk);
+#pragma unroll
+    for (int y = 0; y < NI; ++y) fb[to][y] = rb.read(buf + TM * 128, y, kk);
+  };
+  const auto multiply = [&](int from) {
+#pragma unroll
+    for (int x = 0; x < MI; ++x)
+#pragma unroll
+      for (int y = 0; y < NI; ++y) c[x][y] = mfma32(fb[from][y], fa[from][x], c[x][y]);
+  };
+
+  if (steps > 0) {
+#pragma unroll
+    for (uint32_t s = 0; s < NS; ++s)
+      if (s < steps) load(s);
+    if (steps >= NS) wait_and_meet<(NS - 1) * LOADS>();
+    else wait_and_meet<0>();
+    read(0, 0, 0);
+    for (uint32_t s = 0; s < steps; ++s) {
+      read(s, 1, 1);
+      multiply(0);
+      read(s, 2, 0);
+      multiply(1);
+      read(s, 3, 1);
+      multiply(0);
+      // The next step's tiles are here, and no wave needs this one's again.
+      if (s + NS <= steps) wait_and_meet<(NS - 2) * LOADS>();
+      else wait_and_meet<0>();
+      if (s + NS < steps) load(s + NS);
+      if (s + 1 < steps) read(s + 1, 0, 0);
+      multiply(1);
+    }
+  }
+
+  // A wave turns its blocks through shared memory of its own, 32 rows at a
+  // time, so that C's rows are read and written in whole lines.
+  float* const turn = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
+  float* const partial = t.partial ? t.partial + (size_t)blockIdx.y * g.m * g.n : nullptr;
+  constexpr int ACROSS = TN / 16;   // lanes across the wave's columns, eight each
+#pragma unroll
+  for (int x = 0; x < MI; ++x) {
+#pragma unroll
+    for (int y = 0; y < NI; ++y)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = {c[x][y][4 * q], c[x][y][4 * q + 1], c[x][y][4 * q + 2], c[x][y][4 * q + 3]};
+        *reinterpret_cast<f32x4*>(turn + (lane & 31u) * PITCH + y * 32 + q * 8 + (lane >> 5) * 4u) = v;
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int e = 0; e < 32 * ACROSS / 64; ++e) {
+      const uint32_t r = e * (64 / ACROSS) + lane / ACROSS, col = lane % ACROSS * 8u;
+      f32x8 v;
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + r * PITCH + col);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + r * PITCH + col + 4);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        v[n] = lo[n];
+        v[n + 4] = hi[n];
+      }
+      const uint32_t i = i0 + wi + x * 32u + r, j = j0 + wj + col;
+      if (!partial) epilogue8<T>(g, i, j, v);
+      else if (i < g.m && j < g.n)
+        store8<float>(partial + (size_t)i * g.n + j, v, g.n - j < 8u ? (int)(g.n - j) : 8);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
-// Four waves, each 64 x 64 of the tile. The second operand of the tile takes
-// the matrix instruction's rows, so a lane ends with four neighbouring
-// columns of one row of C: lane l holds row l % 16, columns 4 (l / 16) + 0..3.
-template <typename T, bool A_ROWS_K, bool B_ROWS_K>
-__global__ __launch_bounds__(256) void gemm_kernel(GemmArgs g) {
-  __shared__ __align__(16) T as[kTile * kPitch], bs[kTile * kPitch];
-  const uint32_t tn = cdiv(g.n, kTile), i0 = blockIdx.x / tn * kTile, j0 = blockIdx.x % tn * kTile;
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, wi = (wave >> 1) * 64u, wj = (wave & 1u) * 64u;
-  f32x4 c[4][4];
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-#pragma unroll
-    for (int y = 0; y < 4; ++y) c[x][y] = f32x4(0.0f);
-  for (uint32_t k0 = 0; k0 < g.k; k0 += kDepth) {
-    __syncthreads();
-    stage<T, A_ROWS_K>(as, static_cast<const T*>(g.a), g.lda, i0, g.m, k0, g.k);
-    stage<T, B_ROWS_K>(bs, static_cast<const T*>(g.b), g.ldb, j0, g.n, k0, g.k);
-    __syncthreads();
-    typename Vec<T>::x8 fa[4], fb[4];
-    const uint32_t at = (lane & 15u) * kPitch + (lane >> 4) * 8u;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      fa[x] = *reinterpret_cast<const typename Vec<T>::x8*>(as + (wi + x * 16u) * kPitch + at);
-      fb[x] = *reinterpret_cast<const typename Vec<T>::x8*>(bs + (wj + x * 16u) * kPitch + at);
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) c[x][y] = mfma16(fb[y], fa[x], c[x][y]);
+// The splits' sums in order, then the epilogue.
+template <typename T>
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* partial, int splits) {
+  const uint32_t across = cdiv(g.n, 8);
+  const uint64_t all = (uint64_t)g.m * across, step = (uint64_t)gridDim.x * 256u;
+  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < all; e += step) {
+    const uint32_t i = (uint32_t)(e / across), j = (uint32_t)(e % across) * 8u;
+    const int valid = g.n - j < 8u ? (int)(g.n - j) : 8;
+    f32x8 c = load8(partial + (size_t)i * g.n + j, valid);
+    for (int s = 1; s < splits; ++s) c += load8(partial + ((size_t)s * g.m + i) * g.n + j, valid);
+    epilogue8<T>(g, i, j, c);
   }
-#pragma unroll
-  for (int x = 0; x < 4; ++x)
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-      epilogue4<T>(g, i0 + wi + x * 16u + (lane & 15u), j0 + wj + y * 16u + (lane >> 4) * 4u, c[x][y]);
+}
+
+// Rows copied to a row distance that is a multiple of eight, zero past their end.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_kernel(const T* p, int64_t ld, T* out, uint32_t rows, uint32_t cols) {
+  const uint32_t across = cdiv(cols, 8);
+  const uint64_t all = (uint64_t)rows * across, step = (uint64_t)gridDim.x * 256u;
+  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < all; e += step) {
+    const uint32_t r = (uint32_t)(e / across), j = (uint32_t)(e % across) * 8u;
+    store8<T>(out + e * 8u, load8(p + (int64_t)r * ld + j, cols - j < 8u ? (int)(cols - j) : 8), 8);
+  }
+}
+
+// ---- launches ---------------------------------------------------------------
+
+uint32_t grid_of(uint64_t items) {
+  const uint64_t groups = (items + 255) / 256;
+  return (uint32_t)(groups < 8192 ? (groups ? groups : 1) : 8192);
+}
+
+// Whether the tiles can load an operand as it stands: 16-byte chunks all the
+// way, and a tile's offsets within 32 bits.
+bool loads_as_is(const void* p, int64_t ld, uint32_t contiguous) {
+  return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && contiguous % 8 == 0 && ld < (1 << 22);
+}
+
+size_t padded_bytes(uint32_t rows, uint32_t cols) { return ((size_t)rows * (cdiv(cols, 8) * 8u) * 2u + 255) & ~(size_t)255; }
+
+struct Shape {
+  int tile;         // index into the tile variants
+  uint32_t splits;
+  uint32_t depth;
+};
+
+constexpr uint32_t kCus = 256;
+
+// Tile and splits: the variant whose rounds of workgroups over the CUs cost
+// least.
+Shape shape_of(uint32_t m, uint32_t n, uint32_t k) {
+  Shape s;
+  const uint64_t big = (uint64_t)cdiv(m, 256) * cdiv(n, 256), mid = (uint64_t)cdiv(m, 128) * cdiv(n, 128);
+  s.tile = big >= kCus ? 0 : mid >= kCus / 2 ? 1 : 2;
+  s.splits = 1;
+  s.depth = cdiv(k ? k : 1, kDepth) * kDepth;
+  const uint64_t tiles = s.tile == 0 ? big : s.tile == 1 ? mid : (uint64_t)cdiv(m, 64) * cdiv(n, 64);
+  if (tiles < kCus && k >= 1024) {
+    uint32_t want = (uint32_t)(2 * kCus / tiles), most = k / 512;
+    if (want > most) want = most;
+    if (want > 1) {
+      s.depth = cdiv(cdiv(k, want), kDepth) * kDepth;
+      s.splits = cdiv(k, s.depth);
+    }
+  }
+  return s;
+}
+
+template <typename T, int TM, int TN, int NS>
+hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
+  const GemmArgs& g = t.g;
+  t.tiles_n = cdiv(g.n, TN);
+  t.tiles = cdiv(g.m, TM) * t.tiles_n;
+  const dim3 grid(t.tiles, splits);
+  if (!g.a_rows_k && !g.b_rows_k) tile_kernel<T, TM, TN, NS, false, false><<<grid, 256, 0, stream>>>(t);
+  else if (!g.a_rows_k) tile_kernel<T, TM, TN, NS, false, true><<<grid, 256, 0, stream>>>(t);
+  else tile_kernel<T, TM, TN, NS, true, true><<<grid, 256, 0, stream>>>(t);
+  return hipGetLastError();
 }
 
 template <typename T>
-hipError_t gemm_typed(const GemmArgs& g, hipStream_t stream) {
-  const uint32_t tiles = cdiv(g.m, kTile) * cdiv(g.n, kTile);
-  if (!g.a_rows_k && !g.b_rows_k) gemm_kernel<T, false, false><<<tiles, 256, 0, stream>>>(g);
-  else if (!g.a_rows_k) gemm_kernel<T, false, true><<<tiles, 256, 0, stream>>>(g);
-  else if (g.b_rows_k) gemm_kernel<T, true, true><<<tiles, 256, 0, stream>>>(g);
-  else gemm_kernel<T, true, false><<<tiles, 256, 0, stream>>>(g);
+hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
+  TileArgs t{};
+  t.g = given;
+  GemmArgs& g = t.g;
+  char* space = static_cast<char*>(g.workspace);
+  const auto as_is = [&](const void** p, int64_t* ld, bool rows_k, uint32_t rows, bool whole) {
+    const uint32_t lines = rows_k ? g.k : rows, contiguous = rows_k ? rows : g.k;
+    if (g.k == 0 || loads_as_is(*p, *ld, whole ? 0 : contiguous)) return hipSuccess;
+    const uint32_t across = cdiv(contiguous, 8);
+    pad_kernel<T><<<grid_of((uint64_t)lines * across), 256, 0, stream>>>(
+        static_cast<const T*>(*p), *ld, reinterpret_cast<T*>(space), lines, contiguous);
+    *p = space;
+    *ld = (int64_t)across * 8;
+    space += padded_bytes(lines, contiguous);
+    return hipGetLastError();
+  };
+  hipError_t rc = as_is(&g.a, &g.lda, g.a_rows_k, g.m, g.a_whole);
+  if (rc != hipSuccess) return rc;
+  if ((rc = as_is(&g.b, &g.ldb, g.b_rows_k, g.n, false)) != hipSuccess) return rc;
+  const Shape s = shape_of(g.m, g.n, g.k);
+  t.depth = s.depth;
+  t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;
+  rc = s.tile == 0   ? launch_tiles<T, 256, 256, 2>(t, s.splits, stream)
+       : s.tile == 1 ? launch_tiles<T, 128, 128, 2>(t, s.splits, stream)
+                     : launch_tiles<T, 64, 64, 4>(t, s.splits, stream);
+  if (rc != hipSuccess || s.splits == 1) return rc;
+  join_kernel<T><<<grid_of((uint64_t)g.m * cdiv(g.n, 8)), 256, 0, stream>>>(g, t.partial, (int)s.splits);
   return hipGetLastError();
 }
 
@@ -150,6 +424,12 @@ hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t stream) {
   return dtype == ARX_BF16 ? gemm_typed<__bf16>(g, stream) : gemm_typed<_Float16>(g, stream);
 }
 
-size_t gemm_workspace(uint32_t, uint32_t, uint32_t, bool, bool) { return 0; }
+size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned) {
+  size_t bytes = 0;
+  if (!aligned || (a_rows_k ? m : k) % 8) bytes += a_rows_k ? padded_bytes(k, m) : padded_bytes(m, k);
+  if (!aligned || (b_rows_k ? n : k) % 8) bytes += b_rows_k ? padded_bytes(k, n) : padded_bytes(n, k);
+  const Shape s = shape_of(m, n, k);
+  return bytes + (s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0);
+}
 
 }  // namespace arx

@@ -448,7 +448,7 @@ struct ActGrad {
       for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(z[j]);
     }
     sum[0] += d;
-    if (a.g) store8<T>(static_cast<T*>(a.g) + (size_t)r * a.n + g * 8u, narrow<T>(d), valid);
+    if (a.g) store8<T>(static_cast<T*>(a.g) + (size_t)r * (cdiv(a.n, 8) * 8u) + g * 8u, narrow<T>(d), 8);
   }
 };
 
