@@ -9,6 +9,9 @@
 // rounded once, from the same binary32 value.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "arx_elem.h"
 #include "arx_layer.h"
 
@@ -24,14 +27,30 @@ __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float act_any(int kind, float z) {
+template <int ACT>
+__device__ __forceinline__ void act_each(f32x8& v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = act<ACT>(v[e]);
+}
+
+__device__ __forceinline__ void act8(int kind, f32x8& v) {
   switch (kind) {
-    case ARX_ACT_RELU: return act<ARX_ACT_RELU>(z);
-    case ARX_ACT_GELU: return act<ARX_ACT_GELU>(z);
-    case ARX_ACT_GELU_TANH: return act<ARX_ACT_GELU_TANH>(z);
-    case ARX_ACT_SILU: return act<ARX_ACT_SILU>(z);
-    default: return z;
+    case ARX_ACT_RELU: return act_each<ARX_ACT_RELU>(v);
+    case ARX_ACT_GELU: return act_each<ARX_ACT_GELU>(v);
+    case ARX_ACT_GELU_TANH: return act_each<ARX_ACT_GELU_TANH>(v);
+    case ARX_ACT_SILU: return act_each<ARX_ACT_SILU>(v);
+    default: return;
   }
+}
+
+// f(0), ..., f(N - 1) with constants, so that what they index stays in registers.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each_of(std::make_integer_sequence<int, N>{}, f);
 }
 
 // Eight sums of row i, columns j.. : bias, z, activation, residual, y.
@@ -41,10 +60,7 @@ __device__ __forceinline__ void epilogue8(const GemmArgs& g, uint32_t i, uint32_
   const int valid = g.n - j < 8u ? (int)(g.n - j) : 8;
   if (g.bias) c += widen(load8(static_cast<const T*>(g.bias) + j, valid));
   if (g.z.p) store8<T>(static_cast<T*>(g.z.p) + (int64_t)i * g.z.ld + j, narrow<T>(c), valid);
-  if (g.act != ARX_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = act_any(g.act, c[e]);
-  }
+  act8(g.act, c);
   if (g.residual.p) c += widen(load8(static_cast<const T*>(g.residual.p) + (int64_t)i * g.residual.ld + j, valid));
   store8<T>(static_cast<T*>(g.y.p) + (int64_t)i * g.y.ld + j, narrow<T>(c), valid);
 }
@@ -105,10 +121,10 @@ struct Loader {
     }
   }
 
-  // Depths [k0, k0 + 64) into `lds`; those from k on are zero.
-  __device__ __forceinline__ void load(char* lds, uint32_t k0, uint32_t k, uint32_t wave) const {
+  // Depths [k0, k0 + 64) into `lds`; those from k on (none, if whole) are zero.
+  __device__ __forceinline__ void load(char* lds, uint32_t k0, uint32_t k, uint32_t wave, bool whole) const {
     const char* const at = base + (int64_t)k0 * step;
-    if (k0 + kDepth <= k) {
+    if (whole || k0 + kDepth <= k) {
 #pragma unroll
       for (int q = 0; q < BLOCKS; ++q) {
         if constexpr (ROWS_K) to_lds(at + (int64_t)(q * 4 * LINES) * step + off[0], lds + (q * 4 + wave) * 1024u);
@@ -173,7 +189,33 @@ struct Fragments {
 // are done, then meets the workgroup.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(N % 16 + N / 16 * 0x4000 + 0x0070);   // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Orders what stands since the last call: an LDS read after each matrix
+// instruction, then a share of the loads after each, so that the matrix cores
+// have work while the other queues fill.
+template <int READS, int LOADS, int MFMAS>
+__device__ __forceinline__ void mix() {
+  constexpr int PER = READS > MFMAS / 2 ? (READS * 2 + MFMAS - 1) / MFMAS : 1;   // reads before one
+  constexpr int FIRST = (READS + PER - 1) / PER, REST = MFMAS > FIRST ? MFMAS - FIRST : 0;
+#pragma unroll
+  for (int i = 0; i < FIRST; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // matrix instructions
+    __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);   // LDS reads
+  }
+  if constexpr (LOADS > 0 && REST > 0) {
+    constexpr int SHARE = (LOADS + REST - 1) / REST;
+#pragma unroll
+    for (int i = 0; i < REST; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, SHARE, 0);   // loads
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 struct TileArgs {
@@ -202,7 +244,8 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
 template <typename T, int TM, int TN, int NS, bool A_ROWS_K, bool B_ROWS_K>
 __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
   constexpr int MI = TM / 64, NI = TN / 64, BYTES = (TM + TN) * 128;
-  constexpr int LOADS = TM / 32 + TN / 32, PITCH = TN / 2 + 4;
+  constexpr int LOADS = TM / 32 + TN / 32, READS = MI * (A_ROWS_K ? 2 : 1) + NI * (B_ROWS_K ? 2 : 1);
+  constexpr int PITCH = TN / 2 + 4;
   static_assert(4 * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
   static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
   __shared__ __align__(1024) char lds[NS * BYTES];
@@ -229,10 +272,10 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
     for (int y = 0; y < NI; ++y) c[x][y] = f32x16(0.0f);
   typename Vec<T>::x8 fa[2][MI], fb[2][NI];
 
-  const auto load = [&](uint32_t s) {
+  const auto load = [&](uint32_t s, bool whole) {
     char* const buf = lds + (s % NS) * BYTES;
-    la.load(buf, k_first + s * kDepth, k_last, wave);
-    lb.load(buf + TM * 128, k_first + s * kDepth, k_last, wave);
+    la.load(buf, k_first + s * kDepth, k_last, wave, whole);
+    lb.load(buf + TM * 128, k_first + s * kDepth, k_last, wave, whole);
   };
   const auto read = [&](uint32_t s, int kk, int to) {
     const char* const buf = lds + (s % NS) * BYTES;
@@ -251,33 +294,49 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
   if (steps > 0) {
 #pragma unroll
     for (uint32_t s = 0; s < NS; ++s)
-      if (s < steps) load(s);
+      if (s < steps) load(s, false);
     if (steps >= NS) wait_and_meet<(NS - 1) * LOADS>();
     else wait_and_meet<0>();
     read(0, 0, 0);
-    for (uint32_t s = 0; s < steps; ++s) {
-      read(s, 1, 1);
-      multiply(0);
-      read(s, 2, 0);
-      multiply(1);
-      read(s, 3, 1);
-      multiply(0);
+    const auto three = [&](uint32_t s) {
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk) {
+        read(s, kk + 1, (kk + 1) & 1);
+        multiply(kk & 1);
+        mix<READS, 0, MI * NI>();
+      }
+    };
+    // Where a step behaves as most do: more than the buffers hold ahead of
+    // it, and the tiles that it loads are whole.
+    const uint32_t whole = (k_last - k_first) / kDepth;
+    uint32_t s = 0;
+    for (; s + NS < whole; ++s) {
+      three(s);
       // The next step's tiles are here, and no wave needs this one's again.
-      if (s + NS <= steps) wait_and_meet<(NS - 2) * LOADS>();
-      else wait_and_meet<0>();
-      if (s + NS < steps) load(s + NS);
-      if (s + 1 < steps) read(s + 1, 0, 0);
+      wait_and_meet<(NS - 2) * LOADS>();
+      read(s + 1, 0, 0);
+      load(s + NS, true);
       multiply(1);
+      mix<READS, LOADS, MI * NI>();
+    }
+    for (; s < steps; ++s) {
+      three(s);
+      wait_and_meet<0>();
+      if (s + NS < steps) load(s + NS, false);
+      read(s + 1 < steps ? s + 1 : s, 0, 0);   // the last step's is of no use, and in bounds
+      multiply(1);
+      mix<READS, 0, MI * NI>();
     }
   }
+  wait_and_meet<0>();   // no wave reads the buffers any more
 
   // A wave turns its blocks through shared memory of its own, 32 rows at a
   // time, so that C's rows are read and written in whole lines.
   float* const turn = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
   float* const partial = t.partial ? t.partial + (size_t)blockIdx.y * g.m * g.n : nullptr;
   constexpr int ACROSS = TN / 16;   // lanes across the wave's columns, eight each
-#pragma unroll
-  for (int x = 0; x < MI; ++x) {
+  each<MI>([&](auto at) {
+    constexpr int x = at;
 #pragma unroll
     for (int y = 0; y < NI; ++y)
 #pragma unroll
@@ -286,7 +345,7 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
         *reinterpret_cast<f32x4*>(turn + (lane & 31u) * PITCH + y * 32 + q * 8 + (lane >> 5) * 4u) = v;
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
+#pragma unroll 2
     for (int e = 0; e < 32 * ACROSS / 64; ++e) {
       const uint32_t r = e * (64 / ACROSS) + lane / ACROSS, col = lane % ACROSS * 8u;
       f32x8 v;
@@ -303,7 +362,7 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
         store8<float>(partial + (size_t)i * g.n + j, v, g.n - j < 8u ? (int)(g.n - j) : 8);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  });
 }
 
 // The splits' sums in order, then the epilogue.

@@ -181,11 +181,10 @@ BAD = [
 
 @pytest.mark.parametrize("i", range(len(BAD)))
 def test_binding_refuses(i, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(arx, "_stream", lambda s: 0)
-    monkeypatch.setattr(arx._Call, "empty", lambda self, *shape, dtype=None:
-                        Fake(*shape, dtype=dtype or self.dtype) if len(shape) == 2 and shape[0] != 2 else
-                        torch.empty(shape, dtype=dtype or self.dtype))
+    monkeypatch.setattr(arx, "_current_device", lambda: 0)
+    monkeypatch.setattr(arx, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(arx._Call, "empty", lambda self, shape, dtype=None:
+                        Fake(*shape) if shape != (2, 4) else torch.empty(shape, dtype=dtype))
     call, why = BAD[i]
     with pytest.raises(arx.ArxError) as e:
         call()
