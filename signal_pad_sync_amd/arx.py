@@ -2,9 +2,11 @@
 include/arx_test.h).
 
 Argument marshalling only: every step of the path runs in the library's HIP
-kernels. torch provides device memory and streams; tensors are passed as
+kernels. The layer operators' tensors are checked in compiled code
+(csrc/arx_binding.cpp). torch provides device memory and streams; tensors are passed as
 ``data_ptr()`` and streams as ``torch.cuda.current_stream().cuda_stream``.
-Importing this module raises if libarx.so is missing: there is no fallback.
+Importing this module raises if libarx.so or _binding.so is missing: there is
+no fallback.
 """
 import atexit
 import ctypes
@@ -107,9 +109,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 lib = load()
 import torch  # noqa: E402  (load() has imported it first)
+from signal_pad_sync_amd import _binding  # noqa: E402  (csrc/arx_binding.cpp; needs torch's libraries)
 
-_TYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
-_MATRIX_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
+_binding.bind(ArxError, {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name, _, _ in SIGNATURES})
 
 # The current device and stream, as torch's own compiled code asks for them:
 # torch.cuda.current_stream() costs a call 2.8 us of host time, this 0.1.
@@ -137,10 +139,6 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _buf(t, n: int, what: str, itemsize: int = 2):
@@ -358,84 +356,9 @@ def pad_view(rank: int):
 # ---- layer operators ---------------------------------------------------------
 #
 # Planes are 2-D tensors whose rows are contiguous (stride(1) == 1, any row
-# stride); vectors are contiguous. Outputs that the caller does not pass, and
-# workspaces, come from torch's allocator on the stream of the call.
-
-
-class _Call:
-    """One call's first tensor, type, GPU and stream, and the checks of its
-    other tensors. It costs host time on every call, so it asks each tensor
-    as little as it can."""
-
-    __slots__ = ("first", "dtype", "device", "code", "stream", "alloc")
-
-    def __init__(self, first, what, dtypes, stream):
-        if not getattr(first, "is_cuda", False):
-            raise ArxError(EINVAL, f"{what} must be a GPU tensor")
-        self.first, self.dtype, self.device = first, first.dtype, first.get_device()
-        self.code = dtypes.get(self.dtype)
-        if self.code is None:
-            raise ArxError(EINVAL, f"{what} is {self.dtype}, not one of {[str(d) for d in dtypes]}")
-        if self.device != _current_device():
-            raise ArxError(EINVAL, f"{what} is on GPU {self.device}, not on the current one")
-        if stream is None:
-            self.stream, self.alloc = _current_stream(self.device), None
-        else:
-            self.stream = _stream(stream)
-            self.alloc = torch.cuda.ExternalStream(self.stream)
-
-    def plane(self, t, what, shape=None):
-        """(address, row stride) of a 2-D tensor of the call's type."""
-        if t is None:
-            return None, 0
-        if t.dtype != self.dtype:
-            raise ArxError(EINVAL, f"{what} is {t.dtype}, not {self.dtype}")
-        if t.get_device() != self.device:
-            raise ArxError(EINVAL, f"{what} must be a tensor on the call's GPU")
-        size, strides = t.shape, t.stride()
-        if len(strides) != 2 or (shape is not None and size != shape):
-            raise ArxError(EINVAL, f"{what} has shape {tuple(size)}, not " +
-                           ("two dimensions" if shape is None else f"{tuple(shape)}"))
-        rows, cols = size
-        ld = strides[0]
-        if (strides[1] != 1 and cols > 1) or (ld < cols and rows > 1):
-            raise ArxError(EINVAL, f"{what} has strides {strides}: its rows must be contiguous and apart")
-        return t.data_ptr(), ld if rows > 1 else max(ld, cols)
-
-    def vector(self, t, what, n, dtype=None):
-        """Address of a contiguous vector of n elements."""
-        if t is None:
-            return None
-        if t.dtype != (dtype or self.dtype):
-            raise ArxError(EINVAL, f"{what} is {t.dtype}, not {dtype or self.dtype}")
-        if t.get_device() != self.device:
-            raise ArxError(EINVAL, f"{what} must be a tensor on the call's GPU")
-        size = t.shape
-        if len(size) != 1 or size[0] != n or (n > 1 and t.stride(0) != 1):
-            raise ArxError(EINVAL, f"{what} has shape {tuple(size)} and strides {t.stride()}, not ({n},) and (1,)")
-        return t.data_ptr()
-
-    def empty(self, shape, dtype=None):
-        if self.alloc is None:
-            return self.first.new_empty(shape, dtype=dtype)
-        with torch.cuda.stream(self.alloc):   # its memory is reused in that stream's order
-            return self.first.new_empty(shape, dtype=dtype)
-
-    def workspace(self, nbytes):
-        """(tensor, address); the tensor lives until the call has been queued."""
-        if nbytes == 0:
-            return None, None
-        t = self.empty(nbytes, torch.uint8)
-        return t, t.data_ptr()
-
-
-def _norm_types(weight, shift, dtype):
-    """Type and code of a norm's weight and shift: the rows' or float32."""
-    given = weight if weight is not None else shift
-    wdtype = dtype if given is None else given.dtype
-    if wdtype != dtype and wdtype != torch.float32:
-        raise ArxError(EINVAL, f"weight is {wdtype}, not {dtype} or torch.float32")
-    return wdtype, _TYPES[wdtype]
+# stride); vectors are contiguous; all are on the current device. Outputs that
+# the caller does not pass, and workspaces, come from torch's allocator. Calls
+# run on the current stream, or on `stream`, whose memory the outputs then are.
 
 
 def _act(act):
@@ -444,9 +367,13 @@ def _act(act):
     return ACTS[act]
 
 
-def _on_lines(p, ld):
-    """Rows that all start on 16-byte boundaries (arx.h, arx_linear)."""
-    return not p & 15 and not ld & 7 and ld < 1 << 22
+def _run(op, stream, *args):
+    if stream is None:
+        device = _current_device()
+        return op(device, _current_stream(device), *args)
+    # allocations follow the current stream, so the call's stream becomes it
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream))):
+        return _run(op, None, *args)
 
 
 def linear(x, w, bias=None, residual=None, act="none", save_z=False, out=None, stream=None):
@@ -454,167 +381,50 @@ def linear(x, w, bias=None, residual=None, act="none", save_z=False, out=None, s
     [n], residual [m, n], all bf16 or all f16. Returns y, or (y, z) with
     save_z (what linear_backward needs unless act is "none"). out: a plane for
     y; residual itself will do."""
-    c = _Call(x, "x", _MATRIX_TYPES, stream)
-    kind = _act(act)
-    xp, ldx = c.plane(x, "x")
-    wp, ldw = c.plane(w, "w")
-    m, k = x.shape
-    n = w.shape[0]
-    if w.shape[1] != k:
-        raise ArxError(EINVAL, f"w has shape {tuple(w.shape)} for rows of {k}")
-    rp, ldr = c.plane(residual, "residual", (m, n))
-    if out is None:
-        out = c.empty((m, n))
-    yp, ldy = c.plane(out, "out", (m, n))
-    z = c.empty((m, n)) if save_z else None
-    space = lib.arx_linear_workspace(m, n, k, _on_lines(xp, ldx) and _on_lines(wp, ldw))
-    hold, space_p = c.workspace(space)
-    _check(lib.arx_linear(xp, wp, c.vector(bias, "bias", n), rp, yp, z.data_ptr() if save_z else None, m, n, k, ldx,
-                          ldw, ldr, ldy, n, kind, c.code, space_p, space, c.stream))
-    return (out, z) if save_z else out
+    return _run(_binding.linear, stream, x, w, bias, residual, _act(act), save_z, out)
 
 
 def linear_backward(dy, x, w, z=None, act="none", dx=True, dw=True, dbias=False, stream=None):
     """Gradients of linear: (dx, dw, dbias), None for those not asked for. z
     is what linear gave with save_z. The residual's gradient is dy."""
-    c = _Call(dy, "dy", _MATRIX_TYPES, stream)
-    kind = _act(act)
-    dyp, lddy = c.plane(dy, "dy")
-    m, n = dy.shape
-    xp, ldx = c.plane(x, "x")
-    wp, ldw = c.plane(w, "w")
-    k = w.shape[1]
-    if x.shape != (m, k) or w.shape[0] != n:
-        raise ArxError(EINVAL, f"dy {tuple(dy.shape)}, x {tuple(x.shape)} and w {tuple(w.shape)} do not belong together")
-    if z is None and kind:
-        raise ArxError(EINVAL, f"act {act!r} needs z")
-    zp, ldz = c.plane(z, "z", (m, n)) if kind else (None, 0)
-    gx = c.empty((m, k)) if dx else None
-    gw = c.empty((n, k)) if dw else None
-    gb = c.empty(n) if dbias else None
-    space = lib.arx_linear_backward_workspace(
-        m, n, k, kind, _on_lines(dyp, lddy) and _on_lines(xp, ldx) and _on_lines(wp, ldw))
-    hold, space_p = c.workspace(space)
-    _check(lib.arx_linear_backward(dyp, xp, wp, zp, _ptr(gx), _ptr(gw), _ptr(gb), m, n, k, lddy, ldx, ldw, ldz, k, k,
-                                   kind, c.code, space_p, space, c.stream))
-    return gx, gw, gb
+    return _run(_binding.linear_backward, stream, dy, x, w, z, _act(act), dx, dw, dbias)
 
 
 def layer_norm(x, weight=None, shift=None, eps=1e-5, out=None, stream=None):
     """Layer norm over each row of x [rows, cols]: (y, mean, rstd), the last
     two float32 [rows] for layer_norm_backward. weight, shift [cols]: x's type
     or float32. out: a plane for y; x itself will do."""
-    c = _Call(x, "x", _TYPES, stream)
-    xp, ldx = c.plane(x, "x")
-    rows, cols = x.shape
-    wdtype, wcode = _norm_types(weight, shift, c.dtype)
-    if out is None:
-        out = c.empty((rows, cols))
-    yp, ldy = c.plane(out, "out", (rows, cols))
-    mean, rstd = c.empty((2, rows), torch.float32).unbind(0)
-    _check(lib.arx_layer_norm(xp, c.vector(weight, "weight", cols, wdtype), c.vector(shift, "shift", cols, wdtype), yp,
-                              mean.data_ptr(), rstd.data_ptr(), rows, cols, ldx, ldy, eps, c.code, wcode, c.stream))
-    return out, mean, rstd
+    return _run(_binding.layer_norm, stream, x, weight, shift, eps, out)
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
     """Gradients of layer_norm: (dx, dweight, dshift); the last two in
     weight's type, or dy's without one."""
-    c = _Call(dy, "dy", _TYPES, stream)
-    dyp, lddy = c.plane(dy, "dy")
-    rows, cols = dy.shape
-    xp, ldx = c.plane(x, "x", (rows, cols))
-    wdtype, wcode = _norm_types(weight, None, c.dtype)
-    dx = c.empty((rows, cols))
-    dw, db = c.empty(cols, wdtype), c.empty(cols, wdtype)
-    space = lib.arx_rows_workspace(rows, cols, 2)
-    hold, space_p = c.workspace(space)
-    _check(lib.arx_layer_norm_backward(dyp, xp, c.vector(mean, "mean", rows, torch.float32),
-                                       c.vector(rstd, "rstd", rows, torch.float32),
-                                       c.vector(weight, "weight", cols, wdtype), dx.data_ptr(), dw.data_ptr(),
-                                       db.data_ptr(), rows, cols, lddy, ldx, cols, c.code, wcode, space_p, space,
-                                       c.stream))
-    return dx, dw, db
-
-
-def _seed(seed, offset):
-    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
-        raise ArxError(EINVAL, f"seed {seed} and offset {offset} must be unsigned 64-bit numbers")
+    return _run(_binding.layer_norm_backward, stream, dy, x, mean, rstd, weight)
 
 
 def dropout_add(x, residual=None, bias=None, p=0.0, seed=0, offset=0, out=None, stream=None):
     """residual + dropout(x + bias), the mask drawn from (seed, offset) and the
     element's place (arx.h, arx_dropout_add) and never stored. out: a plane;
     x or residual itself will do."""
-    c = _Call(x, "x", _TYPES, stream)
-    xp, ldx = c.plane(x, "x")
-    rows, cols = x.shape
-    rp, ldr = c.plane(residual, "residual", (rows, cols))
-    _seed(seed, offset)
-    if out is None:
-        out = c.empty((rows, cols))
-    hp, ldh = c.plane(out, "out", (rows, cols))
-    _check(lib.arx_dropout_add(xp, c.vector(bias, "bias", cols), rp, hp, rows, cols, ldx, ldr, ldh, p, seed, offset,
-                               c.code, c.stream))
-    return out
+    return _run(_binding.dropout_add, stream, x, residual, bias, p, seed, offset, out)
 
 
 def dropout_add_backward(dh, p=0.0, seed=0, offset=0, dbias=False, stream=None):
     """Gradients of dropout_add: (dx, dbias), dbias None unless asked for. The
     residual's gradient is dh."""
-    c = _Call(dh, "dh", _TYPES, stream)
-    dhp, lddh = c.plane(dh, "dh")
-    rows, cols = dh.shape
-    _seed(seed, offset)
-    dx = c.empty((rows, cols))
-    db = c.empty(cols) if dbias else None
-    space = lib.arx_rows_workspace(rows, cols, 1) if dbias else 0
-    hold, space_p = c.workspace(space)
-    _check(lib.arx_dropout_add_backward(dhp, dx.data_ptr(), _ptr(db), rows, cols, lddh, cols, p, seed, offset, c.code,
-                                        space_p, space, c.stream))
-    return dx, db
+    return _run(_binding.dropout_add_backward, stream, dh, p, seed, offset, dbias)
 
 
 def dropout_add_norm(x, residual=None, weight=None, shift=None, bias=None, p=0.0, seed=0, offset=0, eps=1e-5,
                      out=None, stream=None):
     """h = residual + dropout(x + bias) and its layer norm in one pass:
     (h, y, mean, rstd). out: a plane for h; x or residual itself will do."""
-    c = _Call(x, "x", _TYPES, stream)
-    xp, ldx = c.plane(x, "x")
-    rows, cols = x.shape
-    rp, ldr = c.plane(residual, "residual", (rows, cols))
-    wdtype, wcode = _norm_types(weight, shift, c.dtype)
-    _seed(seed, offset)
-    h = c.empty((rows, cols)) if out is None else out
-    hp, ldh = c.plane(h, "out", (rows, cols))
-    y = c.empty((rows, cols))
-    mean, rstd = c.empty((2, rows), torch.float32).unbind(0)
-    _check(lib.arx_dropout_add_norm(xp, c.vector(bias, "bias", cols), rp, c.vector(weight, "weight", cols, wdtype),
-                                    c.vector(shift, "shift", cols, wdtype), hp, y.data_ptr(), mean.data_ptr(),
-                                    rstd.data_ptr(), rows, cols, ldx, ldr, ldh, cols, eps, p, seed, offset, c.code,
-                                    wcode, c.stream))
-    return h, y, mean, rstd
+    return _run(_binding.dropout_add_norm, stream, x, residual, weight, shift, bias, p, seed, offset, eps, out)
 
 
 def dropout_add_norm_backward(dy, dh, h, mean, rstd, weight=None, p=0.0, seed=0, offset=0, dbias=False, stream=None):
     """Gradients of dropout_add_norm from y's (dy) and from h's other users
     (dh, or None): (dx, dresidual, dbias, dweight, dshift), dbias None unless
     asked for."""
-    c = _Call(dy, "dy", _TYPES, stream)
-    dyp, lddy = c.plane(dy, "dy")
-    rows, cols = dy.shape
-    dhp, lddh = c.plane(dh, "dh", (rows, cols))
-    hp, ldh = c.plane(h, "h", (rows, cols))
-    wdtype, wcode = _norm_types(weight, None, c.dtype)
-    _seed(seed, offset)
-    dx, dr = c.empty((rows, cols)), c.empty((rows, cols))
-    db = c.empty(cols) if dbias else None
-    dw, ds = c.empty(cols, wdtype), c.empty(cols, wdtype)
-    space = lib.arx_rows_workspace(rows, cols, 3)
-    hold, space_p = c.workspace(space)
-    _check(lib.arx_dropout_add_norm_backward(dyp, dhp, hp, c.vector(mean, "mean", rows, torch.float32),
-                                             c.vector(rstd, "rstd", rows, torch.float32),
-                                             c.vector(weight, "weight", cols, wdtype), dx.data_ptr(), dr.data_ptr(),
-                                             _ptr(db), dw.data_ptr(), ds.data_ptr(), rows, cols, lddy, lddh, ldh, cols,
-                                             cols, p, seed, offset, c.code, wcode, space_p, space, c.stream))
-    return dx, dr, db, dw, ds
+    return _run(_binding.dropout_add_norm_backward, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias)

@@ -2,6 +2,7 @@
 // residual in the epilogue.
 //
 //   tile_kernel   C = A B^T on the matrix cores, tile by tile
+//   rows_kernel   the same for a few rows of A: B streams past once
 //   join_kernel   adds the splits of a long depth, in order
 //   pad_kernel    rows that start off 16-byte boundaries, copied onto them
 //
@@ -365,6 +366,86 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
   });
 }
 
+// ---- a few rows -------------------------------------------------------------
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Up to 16 MT rows of A against 16 rows of B a workgroup, both with the depth
+// contiguous and at any alignment. Bound by reading B once: it goes straight
+// to registers, and the eight waves take the depth's 64-deep chunks in turn,
+// so that one workgroup keeps 64 KiB of B under way; their sums meet in shared
+// memory. A lane reads 32 consecutive bytes of a row, four lanes a whole
+// 128-byte line; the two halves feed two matrix instructions, A's halves the
+// same, so that depths pair up.
+template <typename T, int MT>
+__global__ __launch_bounds__(512) void rows_kernel(GemmArgs g) {
+  constexpr int WAVES = 8, UNROLL = MT == 1 ? 4 : 2, PITCH = 20;
+  typedef typename Vec<T>::x8 x8;
+  __shared__ __align__(16) float lds[WAVES][MT * 16][PITCH];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 16u;
+  const uint32_t j0 = blockIdx.x * 16u;
+  const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r, g.n - 1u) * g.ldb + k_lane;
+  const T* a[MT];
+  f32x4 c[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    a[t] = static_cast<const T*>(g.a) + (int64_t)min(t * 16u + r, g.m - 1u) * g.lda + k_lane;
+    c[t] = f32x4(0.0f);
+  }
+  const uint32_t whole = g.k / 64u;
+  uint32_t s = wave;
+  for (; s + (UNROLL - 1) * WAVES < whole; s += UNROLL * WAVES) {
+    x8 fb[UNROLL][2], fa[UNROLL][MT][2];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fb[u][h] = load8(b + (s + u * WAVES) * 64u + h * 8, 8);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) fa[u][t][h] = load8(a[t] + (s + u * WAVES) * 64u + h * 8, 8);
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) c[t] = mfma16(fb[u][h], fa[u][t][h], c[t]);
+  }
+  for (; s * 64u < g.k; s += WAVES) {
+    const uint32_t k = s * 64u + k_lane;
+    const int valid = k < g.k ? (int)min(16u, g.k - k) : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const x8 fb = load8(b + s * 64u + h * 8, valid - h * 8);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) c[t] = mfma16(fb, load8(a[t] + s * 64u + h * 8, valid - h * 8), c[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(&lds[wave][t * 16 + r][(lane >> 4) * 4u]) = c[t];
+  __syncthreads();
+  const uint32_t i = threadIdx.x >> 1, j = (threadIdx.x & 1u) * 8u;
+  if (i >= MT * 16) return;
+  f32x8 v = f32x8(0.0f);
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const f32x4 lo = *reinterpret_cast<const f32x4*>(&lds[w][i][j]), hi = *reinterpret_cast<const f32x4*>(&lds[w][i][j + 4]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] += lo[e];
+      v[e + 4] += hi[e];
+    }
+  }
+  epilogue8<T>(g, i, j0 + j, v);
+}
+
 // The splits' sums in order, then the epilogue.
 template <typename T>
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* partial, int splits) {
@@ -445,8 +526,20 @@ hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rows of A up to which B streaming past whole beats tiles.
+constexpr uint32_t kFewRows = 64;
+
+bool few_rows(uint32_t m, bool a_rows_k, bool b_rows_k) { return m <= kFewRows && !a_rows_k && !b_rows_k; }
+
 template <typename T>
 hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
+  if (few_rows(given.m, given.a_rows_k, given.b_rows_k)) {
+    const uint32_t groups = cdiv(given.n, 16);
+    if (given.m <= 16) rows_kernel<T, 1><<<groups, 512, 0, stream>>>(given);
+    else if (given.m <= 32) rows_kernel<T, 2><<<groups, 512, 0, stream>>>(given);
+    else rows_kernel<T, 4><<<groups, 512, 0, stream>>>(given);
+    return hipGetLastError();
+  }
   TileArgs t{};
   t.g = given;
   GemmArgs& g = t.g;
@@ -484,6 +577,7 @@ hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t stream) {
 }
 
 size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned) {
+  if (few_rows(m, a_rows_k, b_rows_k)) return 0;
   size_t bytes = 0;
   if (!aligned || (a_rows_k ? m : k) % 8) bytes += a_rows_k ? padded_bytes(k, m) : padded_bytes(m, k);
   if (!aligned || (b_rows_k ? n : k) % 8) bytes += b_rows_k ? padded_bytes(k, n) : padded_bytes(n, k);

@@ -132,50 +132,46 @@ def test_workspace_sizes():
     assert gelu >= plain + 100 * 64 * 2
 
 
-class Fake:
-    """A tensor's attributes without a GPU."""
-
-    def __init__(self, *shape, dtype=torch.bfloat16, strides=None, device=0, cuda=True):
-        self.shape, self.dtype, self.is_cuda, self._device = torch.Size(shape), dtype, cuda, device
-        self._strides = strides or tuple(torch.empty(shape, device="meta").stride())
-
-    def stride(self, i=None):
-        return self._strides if i is None else self._strides[i]
-
-    def dim(self):
-        return len(self.shape)
-
-    def get_device(self):
-        return self._device
-
-    def data_ptr(self):
-        return A
+def T(*shape, dtype=torch.bfloat16, strides=None):
+    """A CPU tensor: the binding looks at types and shapes first, so every
+    other refusal shows without a GPU, and it is refused for its device last."""
+    return torch.empty_strided(shape, strides, dtype=dtype) if strides else torch.empty(shape, dtype=dtype)
 
 
+F16, F32, I16 = torch.float16, torch.float32, torch.int16
+V = T(4, dtype=F32)
 BAD = [
-    (lambda: arx.linear(Fake(4, 8, cuda=False), Fake(8, 8)), "GPU tensor"),
-    (lambda: arx.linear(Fake(4, 8, dtype=torch.float32), Fake(8, 8)), "float32"),
-    (lambda: arx.linear(Fake(4, 8, device=1), Fake(8, 8)), "GPU 1"),
-    (lambda: arx.linear(Fake(4, 8), Fake(8, 8, dtype=torch.float16)), "w is"),
-    (lambda: arx.linear(Fake(4, 8), Fake(8, 9)), "rows of 8"),
-    (lambda: arx.linear(Fake(4, 8), Fake(8, 8), act="swish"), "act"),
-    (lambda: arx.linear(Fake(2, 4, 8), Fake(8, 8)), "two dimensions"),
-    (lambda: arx.linear(Fake(4, 8, strides=(1, 4)), Fake(8, 8)), "strides"),
-    (lambda: arx.linear(Fake(4, 8, strides=(0, 1)), Fake(8, 8)), "strides"),
-    (lambda: arx.linear(Fake(4, 8), Fake(8, 8), residual=Fake(8), out=Fake(4, 8)), "residual"),
-    (lambda: arx.linear(Fake(4, 8), Fake(6, 8), residual=Fake(1, 6), out=Fake(4, 6)), "residual"),
-    (lambda: arx.linear(Fake(4, 8), Fake(6, 8), bias=Fake(8), out=Fake(4, 6)), "bias"),
-    (lambda: arx.linear(Fake(4, 8), Fake(6, 8), out=Fake(4, 7)), "out"),
-    (lambda: arx.linear_backward(Fake(4, 6), Fake(4, 8), Fake(7, 8)), "belong together"),
-    (lambda: arx.linear_backward(Fake(4, 6), Fake(4, 8), Fake(6, 8), act="gelu"), "needs z"),
-    (lambda: arx.layer_norm(Fake(4, 8), Fake(8, dtype=torch.float16), out=Fake(4, 8)), "weight is"),
-    (lambda: arx.layer_norm(Fake(4, 8, dtype=torch.int16)), "int16"),
-    (lambda: arx.layer_norm_backward(Fake(4, 8), Fake(5, 8), Fake(4), Fake(4)), "x has shape"),
-    (lambda: arx.dropout_add(Fake(4, 8), seed=-1), "seed"),
-    (lambda: arx.dropout_add(Fake(4, 8), offset=1 << 64), "offset"),
-    (lambda: arx.dropout_add(Fake(4, 8), Fake(4, 9)), "residual"),
-    (lambda: arx.dropout_add_norm(Fake(4, 8), None, Fake(8), Fake(8, dtype=torch.float32), out=Fake(4, 8)), ""),
-    (lambda: arx.dropout_add_norm_backward(Fake(4, 8), Fake(3, 8), Fake(4, 8), Fake(4), Fake(4)), "dh"),
+    (lambda: arx.linear(T(4, 8), T(6, 8)), "w must be a GPU tensor"),
+    (lambda: arx.linear(None, T(6, 8)), "x must be a tensor"),
+    (lambda: arx.linear(T(4, 8, dtype=F32), T(8, 8)), "Float"),
+    (lambda: arx.linear(T(4, 8), T(8, 8, dtype=F16)), "w is of type"),
+    (lambda: arx.linear(T(4, 8), T(8, 9)), "w has shape"),
+    (lambda: arx.linear(T(4, 8), T(8)), "w has shape"),
+    (lambda: arx.linear(T(4, 8), T(8, 8), act="swish"), "act"),
+    (lambda: arx.linear(T(2, 4, 8), T(8, 8)), "two dimensions"),
+    (lambda: arx.linear(T(4, 8), T(8, 8, strides=(1, 8))), "contiguous"),
+    (lambda: arx.linear(T(4, 8), T(8, 8, strides=(0, 1))), "contiguous"),
+    (lambda: arx.linear_backward(T(4, 6), T(4, 8), T(7, 8)), "w has shape"),
+    (lambda: arx.linear_backward(T(4, 6), T(5, 8), T(6, 8)), "GPU tensor"),
+    (lambda: arx.layer_norm(T(4, 8), T(8, dtype=F16)), "weight is of type"),
+    (lambda: arx.layer_norm(T(4, 8), None, T(8, dtype=F16)), "shift is of type"),
+    (lambda: arx.layer_norm(T(4, 8, dtype=F32), T(8)), "weight is of type"),
+    (lambda: arx.layer_norm(T(4, 8), T(9)), "weight has shape"),
+    (lambda: arx.layer_norm(T(4, 8), T(8, strides=(2,))), "weight has shape"),
+    (lambda: arx.layer_norm(T(4, 8, dtype=I16)), "Short"),
+    (lambda: arx.layer_norm(T(4, 8), out=T(4, 9)), "out has shape"),
+    (lambda: arx.layer_norm_backward(T(4, 8), T(5, 8), V, V), "x has shape"),
+    (lambda: arx.dropout_add(T(4, 8), seed=-1), "seed"),
+    (lambda: arx.dropout_add(T(4, 8), seed=1.5), "seed"),
+    (lambda: arx.dropout_add(T(4, 8), offset=1 << 64), "offset"),
+    (lambda: arx.dropout_add(T(4, 8), T(4, 9)), "residual has shape"),
+    (lambda: arx.dropout_add(T(4, 8), T(1, 8)), "residual has shape"),
+    (lambda: arx.dropout_add(T(4, 8), T(4, 8, dtype=F16)), "residual is of type"),
+    (lambda: arx.dropout_add(T(4, 8), None, T(9)), "bias has shape"),
+    (lambda: arx.dropout_add_backward(T(4, 8), offset=-1), "offset"),
+    (lambda: arx.dropout_add_norm(T(4, 8), None, T(8), T(8, dtype=F32)), "GPU tensor"),
+    (lambda: arx.dropout_add_norm_backward(T(4, 8), T(3, 8), T(4, 8), V, V), "dh has shape"),
+    (lambda: arx.dropout_add_norm_backward(T(4, 8), None, T(3, 8), V, V), "h has shape"),
 ]
 
 
@@ -183,12 +179,17 @@ BAD = [
 def test_binding_refuses(i, monkeypatch):
     monkeypatch.setattr(arx, "_current_device", lambda: 0)
     monkeypatch.setattr(arx, "_current_stream", lambda device: 0)
-    monkeypatch.setattr(arx._Call, "empty", lambda self, shape, dtype=None:
-                        Fake(*shape) if shape != (2, 4) else torch.empty(shape, dtype=dtype))
     call, why = BAD[i]
     with pytest.raises(arx.ArxError) as e:
         call()
     assert e.value.code == arx.EINVAL and why in str(e.value)
+
+
+def test_binding_refuses_a_wrong_count():
+    with pytest.raises(arx.ArxError):
+        arx._binding.linear(0, 0, T(4, 8))
+    with pytest.raises(TypeError):
+        arx._binding.bind(arx.ArxError)
 
 
 @pytest.mark.parametrize("src", ["arx_rows.hip", "arx_linear.hip"])
