@@ -88,10 +88,10 @@ __device__ __forceinline__ void to_lds(const void* p, char* block) {
   __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)block, 16, 0, 0);
 }
 
-// What a wave loads of one operand's tile: block q * 4 + wave of 1 KiB.
-template <typename T, int TILE, bool ROWS_K>
+// What one of NW waves loads of one operand's tile: block q * NW + wave of 1 KiB.
+template <typename T, int TILE, bool ROWS_K, int NW>
 struct Loader {
-  static constexpr int BLOCKS = TILE / 32;   // per wave
+  static constexpr int BLOCKS = TILE / 8 / NW;   // per wave
   static constexpr int LINES = ROWS_K ? 512 / TILE : 8;   // lines of a block: depths or rows
   uint32_t off[ROWS_K ? 1 : BLOCKS];         // byte offset of this lane's chunk
   uint32_t line;                             // first depth (ROWS_K) or first chunk of this lane
@@ -113,7 +113,7 @@ struct Loader {
       line = (lane & 7u) ^ (lane >> 3);
 #pragma unroll
       for (int q = 0; q < BLOCKS; ++q) {
-        uint32_t r = (q * 4 + wave) * 8u + (lane >> 3);
+        uint32_t r = (q * NW + wave) * 8u + (lane >> 3);
         if (r >= rows - r0) r = rows - r0 - 1u;
         off[q] = (uint32_t)(r * ld * sizeof(T)) + line * 16u;
       }
@@ -128,18 +128,18 @@ struct Loader {
     if (whole || k0 + kDepth <= k) {
 #pragma unroll
       for (int q = 0; q < BLOCKS; ++q) {
-        if constexpr (ROWS_K) to_lds(at + (int64_t)(q * 4 * LINES) * step + off[0], lds + (q * 4 + wave) * 1024u);
-        else to_lds(at + off[q], lds + (q * 4 + wave) * 1024u);
+        if constexpr (ROWS_K) to_lds(at + (int64_t)(q * NW * LINES) * step + off[0], lds + (q * NW + wave) * 1024u);
+        else to_lds(at + off[q], lds + (q * NW + wave) * 1024u);
       }
     } else {
 #pragma unroll
       for (int q = 0; q < BLOCKS; ++q) {
         const char* src;
         if constexpr (ROWS_K)
-          src = k0 + q * 4 * LINES + line < k ? at + (int64_t)(q * 4 * LINES) * step + off[0] : nullptr;
+          src = k0 + q * NW * LINES + line < k ? at + (int64_t)(q * NW * LINES) * step + off[0] : nullptr;
         else
           src = k0 + line * 8u < k ? at + off[q] : nullptr;
-        to_lds(src ? src : reinterpret_cast<const char*>(&kZeros), lds + (q * 4 + wave) * 1024u);
+        to_lds(src ? src : reinterpret_cast<const char*>(&kZeros), lds + (q * NW + wave) * 1024u);
       }
     }
   }
@@ -238,28 +238,29 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
   *tj = in / high;
 }
 
-// C's TM x TN tile on four waves, each (TM / 2) x (TN / 2) in 32 x 32 blocks.
+// C's TM x TN tile on WM x WN waves, each in 32 x 32 blocks.
 // The depth runs through NS buffers: while the matrix cores work on one, the
 // loads of the next NS - 1 are under way. B's fragments take the matrix
 // instruction's rows, so a lane's sums are neighbours in a row of C.
-template <typename T, int TM, int TN, int NS, bool A_ROWS_K, bool B_ROWS_K>
-__global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
-  constexpr int MI = TM / 64, NI = TN / 64, BYTES = (TM + TN) * 128;
-  constexpr int LOADS = TM / 32 + TN / 32, READS = MI * (A_ROWS_K ? 2 : 1) + NI * (B_ROWS_K ? 2 : 1);
-  constexpr int PITCH = TN / 2 + 4;
-  static_assert(4 * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
+template <typename T, int TM, int TN, int WM, int WN, int NS, bool A_ROWS_K, bool B_ROWS_K>
+__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+  constexpr int NW = WM * WN, MI = TM / WM / 32, NI = TN / WN / 32, BYTES = (TM + TN) * 128;
+  constexpr int LOADS = (TM + TN) / 8 / NW, READS = MI * (A_ROWS_K ? 2 : 1) + NI * (B_ROWS_K ? 2 : 1);
+  constexpr int PITCH = TN / WN + 4;
+  static_assert(!A_ROWS_K || TM >= 64, "four 32-byte pieces to a line");
+  static_assert(NW * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
   static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
   __shared__ __align__(1024) char lds[NS * BYTES];
   const GemmArgs& g = t.g;
   uint32_t ti, tj;
   tile_of(blockIdx.x, t.tiles, t.tiles_n, &ti, &tj);
   const uint32_t i0 = ti * TM, j0 = tj * TN, lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = (wave >> 1) * (TM / 2),
-                 wj = (wave & 1u) * (TN / 2);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = wave / WN * (TM / WM),
+                 wj = wave % WN * (TN / WN);
   const uint32_t k_first = blockIdx.y * t.depth, k_last = min(g.k, k_first + t.depth);
   const uint32_t steps = k_last > k_first ? (k_last - k_first + kDepth - 1) / kDepth : 0u;
-  Loader<T, TM, A_ROWS_K> la;
-  Loader<T, TN, B_ROWS_K> lb;
+  Loader<T, TM, A_ROWS_K, NW> la;
+  Loader<T, TN, B_ROWS_K, NW> lb;
   la.init(g.a, g.lda, i0, g.m, wave);
   lb.init(g.b, g.ldb, j0, g.n, wave);
   Fragments<T, TM, A_ROWS_K> ra;
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(256) void tile_kernel(TileArgs t) {
   // time, so that C's rows are read and written in whole lines.
   float* const turn = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
   float* const partial = t.partial ? t.partial + (size_t)blockIdx.y * g.m * g.n : nullptr;
-  constexpr int ACROSS = TN / 16;   // lanes across the wave's columns, eight each
+  constexpr int ACROSS = TN / WN / 8;   // lanes across the wave's columns, eight each
   each<MI>([&](auto at) {
     constexpr int x = at;
 #pragma unroll
@@ -375,21 +376,22 @@ __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Up to 16 MT rows of A against 16 rows of B a workgroup, both with the depth
+// Up to 16 MT rows of A against ROWS rows of B a workgroup (8: the matrix
+// instruction's other rows repeat them), both with the depth
 // contiguous and at any alignment. Bound by reading B once: it goes straight
-// to registers, and the eight waves take the depth's 64-deep chunks in turn,
-// so that one workgroup keeps 64 KiB of B under way; their sums meet in shared
-// memory. A lane reads 32 consecutive bytes of a row, four lanes a whole
-// 128-byte line; the two halves feed two matrix instructions, A's halves the
-// same, so that depths pair up.
-template <typename T, int MT>
-__global__ __launch_bounds__(512) void rows_kernel(GemmArgs g) {
-  constexpr int WAVES = 8, UNROLL = MT == 1 ? 4 : 2, PITCH = 20;
+// to registers, and the sixteen waves take the depth's 64-deep chunks in turn,
+// so that a workgroup has all of a common depth under way at once; their sums
+// meet in shared memory. Four lanes read 64 consecutive bytes of a row.
+template <typename T, int MT, int ROWS>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs ta) {
+  const GemmArgs& g = ta.g;
+  constexpr int WAVES = 16, UNROLL = MT == 4 ? 2 : 4, PITCH = 20;
   typedef typename Vec<T>::x8 x8;
   __shared__ __align__(16) float lds[WAVES][MT * 16][PITCH];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 16u;
-  const uint32_t j0 = blockIdx.x * 16u;
-  const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r, g.n - 1u) * g.ldb + k_lane;
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 8u;
+  const uint32_t j0 = blockIdx.x * ROWS;
+  const uint32_t k_first = blockIdx.y * ta.depth, k_end = min(g.k, k_first + ta.depth);
+  const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r % ROWS, g.n - 1u) * g.ldb + k_lane;
   const T* a[MT];
   f32x4 c[MT];
 #pragma unroll
@@ -397,20 +399,21 @@ __global__ __launch_bounds__(512) void rows_kernel(GemmArgs g) {
     a[t] = static_cast<const T*>(g.a) + (int64_t)min(t * 16u + r, g.m - 1u) * g.lda + k_lane;
     c[t] = f32x4(0.0f);
   }
-  const uint32_t whole = g.k / 64u;
-  uint32_t s = wave;
+  const uint32_t whole = k_end / 64u;
+  uint32_t s = k_first / 64u + wave;
   for (; s + (UNROLL - 1) * WAVES < whole; s += UNROLL * WAVES) {
     x8 fb[UNROLL][2], fa[UNROLL][MT][2];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fb[u][h] = load8(b + (s + u * WAVES) * 64u + h * 8, 8);
+      for (int h = 0; h < 2; ++h) fb[u][h] = load8(b + (s + u * WAVES) * 64u + h * 32, 8);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) fa[u][t][h] = load8(a[t] + (s + u * WAVES) * 64u + h * 8, 8);
+        for (int h = 0; h < 2; ++h) fa[u][t][h] = load8(a[t] + (s + u * WAVES) * 64u + h * 32, 8);
+    __builtin_amdgcn_sched_barrier(0);   // every load is under way before the first product waits
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
@@ -418,20 +421,20 @@ __global__ __launch_bounds__(512) void rows_kernel(GemmArgs g) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) c[t] = mfma16(fb[u][h], fa[u][t][h], c[t]);
   }
-  for (; s * 64u < g.k; s += WAVES) {
-    const uint32_t k = s * 64u + k_lane;
-    const int valid = k < g.k ? (int)min(16u, g.k - k) : 0;
+  for (; s * 64u < k_end; s += WAVES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const x8 fb = load8(b + s * 64u + h * 8, valid - h * 8);
+      const uint32_t k = s * 64u + h * 32u + k_lane;
+      const int valid = k < k_end ? (int)min(8u, k_end - k) : 0;
+      const x8 fb = load8(b + s * 64u + h * 32, valid);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) c[t] = mfma16(fb, load8(a[t] + s * 64u + h * 8, valid - h * 8), c[t]);
+      for (int t = 0; t < MT; ++t) c[t] = mfma16(fb, load8(a[t] + s * 64u + h * 32, valid), c[t]);
     }
   }
 #pragma unroll
   for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(&lds[wave][t * 16 + r][(lane >> 4) * 4u]) = c[t];
   __syncthreads();
-  const uint32_t i = threadIdx.x >> 1, j = (threadIdx.x & 1u) * 8u;
+  const uint32_t i = threadIdx.x / (ROWS / 8), j = threadIdx.x % (ROWS / 8) * 8u;
   if (i >= MT * 16) return;
   f32x8 v = f32x8(0.0f);
 #pragma unroll
@@ -443,7 +446,10 @@ __global__ __launch_bounds__(512) void rows_kernel(GemmArgs g) {
       v[e + 4] += hi[e];
     }
   }
-  epilogue8<T>(g, i, j0 + j, v);
+  if (!ta.partial) epilogue8<T>(g, i, j0 + j, v);
+  else if (i < g.m && j0 + j < g.n)
+    store8<float>(ta.partial + ((size_t)blockIdx.y * g.m + i) * g.n + j0 + j, v,
+                  g.n - j0 - j < 8u ? (int)(g.n - j0 - j) : 8);
 }
 
 // The splits' sums in order, then the epilogue.
@@ -486,63 +492,58 @@ bool loads_as_is(const void* p, int64_t ld, uint32_t contiguous) {
 
 size_t padded_bytes(uint32_t rows, uint32_t cols) { return ((size_t)rows * (cdiv(cols, 8) * 8u) * 2u + 255) & ~(size_t)255; }
 
+// How a product is cut: the kernel, and workgroups along the depth.
+enum Cut { ROWS8, ROWS16, T32x128, T64x64, T64x128, T128x128, T256x256, CUTS };
 struct Shape {
-  int tile;         // index into the tile variants
+  int cut;
   uint32_t splits;
-  uint32_t depth;
+  uint32_t depth;   // of one split, a multiple of 64
 };
 
 constexpr uint32_t kCus = 256;
 
-// Tile and splits: the variant whose rounds of workgroups over the CUs cost
-// least.
-Shape shape_of(uint32_t m, uint32_t n, uint32_t k) {
+Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
   Shape s;
   const uint64_t big = (uint64_t)cdiv(m, 256) * cdiv(n, 256), mid = (uint64_t)cdiv(m, 128) * cdiv(n, 128);
-  s.tile = big >= kCus ? 0 : mid >= kCus / 2 ? 1 : 2;
+  s.cut = big >= kCus ? T256x256 : mid >= kCus / 2 ? T128x128 : T64x64;
   s.splits = 1;
-  s.depth = cdiv(k ? k : 1, kDepth) * kDepth;
-  const uint64_t tiles = s.tile == 0 ? big : s.tile == 1 ? mid : (uint64_t)cdiv(m, 64) * cdiv(n, 64);
+  uint64_t tiles = s.cut == T256x256 ? big : s.cut == T128x128 ? mid : (uint64_t)cdiv(m, 64) * cdiv(n, 64);
+  if (m <= 16 && !a_rows_k && !b_rows_k) s.cut = ROWS16, tiles = kCus;
   if (tiles < kCus && k >= 1024) {
     uint32_t want = (uint32_t)(2 * kCus / tiles), most = k / 512;
     if (want > most) want = most;
-    if (want > 1) {
-      s.depth = cdiv(cdiv(k, want), kDepth) * kDepth;
-      s.splits = cdiv(k, s.depth);
-    }
+    if (want > 1) s.splits = want;
   }
+  s.depth = cdiv(cdiv(k ? k : 1, s.splits), kDepth) * kDepth;
+  s.splits = cdiv(k ? k : 1, s.depth);
   return s;
 }
 
-template <typename T, int TM, int TN, int NS>
+template <typename T, int TM, int TN, int WM, int WN, int NS>
 hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
   const GemmArgs& g = t.g;
   t.tiles_n = cdiv(g.n, TN);
   t.tiles = cdiv(g.m, TM) * t.tiles_n;
   const dim3 grid(t.tiles, splits);
-  if (!g.a_rows_k && !g.b_rows_k) tile_kernel<T, TM, TN, NS, false, false><<<grid, 256, 0, stream>>>(t);
-  else if (!g.a_rows_k) tile_kernel<T, TM, TN, NS, false, true><<<grid, 256, 0, stream>>>(t);
-  else tile_kernel<T, TM, TN, NS, true, true><<<grid, 256, 0, stream>>>(t);
+  if (!g.a_rows_k && !g.b_rows_k) tile_kernel<T, TM, TN, WM, WN, NS, false, false><<<grid, WM * WN * 64, 0, stream>>>(t);
+  else if (!g.a_rows_k) tile_kernel<T, TM, TN, WM, WN, NS, false, true><<<grid, WM * WN * 64, 0, stream>>>(t);
+  else if constexpr (TM >= 64) tile_kernel<T, TM, TN, WM, WN, NS, true, true><<<grid, WM * WN * 64, 0, stream>>>(t);
   return hipGetLastError();
 }
 
-// Rows of A up to which B streaming past whole beats tiles.
-constexpr uint32_t kFewRows = 64;
-
-bool few_rows(uint32_t m, bool a_rows_k, bool b_rows_k) { return m <= kFewRows && !a_rows_k && !b_rows_k; }
+template <typename T, int ROWS>
+hipError_t launch_rows(const TileArgs& t, uint32_t splits, hipStream_t stream) {
+  rows_kernel<T, 1, ROWS><<<dim3(cdiv(t.g.n, ROWS), splits), 1024, 0, stream>>>(t);
+  return hipGetLastError();
+}
 
 template <typename T>
 hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
-  if (few_rows(given.m, given.a_rows_k, given.b_rows_k)) {
-    const uint32_t groups = cdiv(given.n, 16);
-    if (given.m <= 16) rows_kernel<T, 1><<<groups, 512, 0, stream>>>(given);
-    else if (given.m <= 32) rows_kernel<T, 2><<<groups, 512, 0, stream>>>(given);
-    else rows_kernel<T, 4><<<groups, 512, 0, stream>>>(given);
-    return hipGetLastError();
-  }
   TileArgs t{};
   t.g = given;
   GemmArgs& g = t.g;
+  const Shape s = shape_of(g.m, g.n, g.k, g.a_rows_k, g.b_rows_k);
+  hipError_t rc = hipSuccess;
   char* space = static_cast<char*>(g.workspace);
   const auto as_is = [&](const void** p, int64_t* ld, bool rows_k, uint32_t rows, bool whole) {
     const uint32_t lines = rows_k ? g.k : rows, contiguous = rows_k ? rows : g.k;
@@ -555,15 +556,21 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
     space += padded_bytes(lines, contiguous);
     return hipGetLastError();
   };
-  hipError_t rc = as_is(&g.a, &g.lda, g.a_rows_k, g.m, g.a_whole);
-  if (rc != hipSuccess) return rc;
-  if ((rc = as_is(&g.b, &g.ldb, g.b_rows_k, g.n, false)) != hipSuccess) return rc;
-  const Shape s = shape_of(g.m, g.n, g.k);
+  if (s.cut > ROWS16) {   // the tiles' loads go by whole chunks
+    if ((rc = as_is(&g.a, &g.lda, g.a_rows_k, g.m, g.a_whole)) != hipSuccess) return rc;
+    if ((rc = as_is(&g.b, &g.ldb, g.b_rows_k, g.n, false)) != hipSuccess) return rc;
+  }
   t.depth = s.depth;
   t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;
-  rc = s.tile == 0   ? launch_tiles<T, 256, 256, 2>(t, s.splits, stream)
-       : s.tile == 1 ? launch_tiles<T, 128, 128, 2>(t, s.splits, stream)
-                     : launch_tiles<T, 64, 64, 4>(t, s.splits, stream);
+  switch (s.cut) {
+    case ROWS8: rc = launch_rows<T, 8>(t, s.splits, stream); break;
+    case ROWS16: rc = launch_rows<T, 16>(t, s.splits, stream); break;
+    case T32x128: rc = launch_tiles<T, 32, 128, 1, 4, 4>(t, s.splits, stream); break;
+    case T64x64: rc = launch_tiles<T, 64, 64, 2, 2, 4>(t, s.splits, stream); break;
+    case T64x128: rc = launch_tiles<T, 64, 128, 2, 2, 3>(t, s.splits, stream); break;
+    case T128x128: rc = launch_tiles<T, 128, 128, 2, 2, 2>(t, s.splits, stream); break;
+    default: rc = launch_tiles<T, 256, 256, 2, 4, 2>(t, s.splits, stream); break;
+  }
   if (rc != hipSuccess || s.splits == 1) return rc;
   join_kernel<T><<<grid_of((uint64_t)g.m * cdiv(g.n, 8)), 256, 0, stream>>>(g, t.partial, (int)s.splits);
   return hipGetLastError();
@@ -577,12 +584,12 @@ hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t stream) {
 }
 
 size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned) {
-  if (few_rows(m, a_rows_k, b_rows_k)) return 0;
-  size_t bytes = 0;
+  const Shape s = shape_of(m, n, k, a_rows_k, b_rows_k);
+  size_t bytes = s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0;
+  if (s.cut <= ROWS16) return bytes;
   if (!aligned || (a_rows_k ? m : k) % 8) bytes += a_rows_k ? padded_bytes(k, m) : padded_bytes(m, k);
   if (!aligned || (b_rows_k ? n : k) % 8) bytes += b_rows_k ? padded_bytes(k, n) : padded_bytes(n, k);
-  const Shape s = shape_of(m, n, k);
-  return bytes + (s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0);
+  return bytes;
 }
 
 }  // namespace arx
