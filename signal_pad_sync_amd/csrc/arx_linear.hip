@@ -80,12 +80,19 @@ constexpr int kDepth = 64;
 // Sixteen zero bytes that lanes past the end of the depth read instead.
 __device__ const uint4 kZeros = {0, 0, 0, 0};
 
-typedef const __attribute__((address_space(1))) void* GlobalPtr;
-typedef __attribute__((address_space(3))) void* LdsPtr;
-
-// One lane's 16 bytes from p to the wave's 1 KiB block at LDS offset `block`.
-__device__ __forceinline__ void to_lds(const void* p, char* block) {
-  __builtin_amdgcn_global_load_lds((GlobalPtr)p, (LdsPtr)block, 16, 0, 0);
+// One lane's 16 bytes to its place in the wave's 1 KiB block at LDS address
+// `block`, from base + off or from p. The builtin for this makes the compiler
+// wait for every LDS read under way at the next use of any; the instruction
+// itself has no result register, and the waits for it are written out
+// (wait_and_meet). It stays between the statements that it stands between.
+__device__ __forceinline__ void to_lds(const char* base, uint32_t off, uint32_t block) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(block), "v"(off), "s"(base) : "m0");
+}
+__device__ __forceinline__ void to_lds(const void* p, uint32_t block) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(block), "v"(p) : "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
 // What one of NW waves loads of one operand's tile: block q * NW + wave of 1 KiB.
@@ -122,25 +129,22 @@ struct Loader {
     }
   }
 
-  // Depths [k0, k0 + 64) into `lds`; those from k on (none, if whole) are zero.
-  __device__ __forceinline__ void load(char* lds, uint32_t k0, uint32_t k, uint32_t wave, bool whole) const {
+  // Block q of the depths [k0, k0 + 64), all there, into the tile at `lds`.
+  __device__ __forceinline__ void load(uint32_t lds, uint32_t k0, int q, uint32_t wave) const {
     const char* const at = base + (int64_t)k0 * step;
-    if (whole || k0 + kDepth <= k) {
+    if constexpr (ROWS_K) to_lds(at + (int64_t)(q * NW * LINES) * step, off[0], lds + (q * NW + wave) * 1024u);
+    else to_lds(at, off[q], lds + (q * NW + wave) * 1024u);
+  }
+
+  // All blocks of the depths [k0, k0 + 64), those from k on zero.
+  __device__ __forceinline__ void load_end(uint32_t lds, uint32_t k0, uint32_t k, uint32_t wave) const {
+    const char* const at = base + (int64_t)k0 * step;
 #pragma unroll
-      for (int q = 0; q < BLOCKS; ++q) {
-        if constexpr (ROWS_K) to_lds(at + (int64_t)(q * NW * LINES) * step + off[0], lds + (q * NW + wave) * 1024u);
-        else to_lds(at + off[q], lds + (q * NW + wave) * 1024u);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < BLOCKS; ++q) {
-        const char* src;
-        if constexpr (ROWS_K)
-          src = k0 + q * NW * LINES + line < k ? at + (int64_t)(q * NW * LINES) * step + off[0] : nullptr;
-        else
-          src = k0 + line * 8u < k ? at + off[q] : nullptr;
-        to_lds(src ? src : reinterpret_cast<const char*>(&kZeros), lds + (q * NW + wave) * 1024u);
-      }
+    for (int q = 0; q < BLOCKS; ++q) {
+      const char* src;
+      if constexpr (ROWS_K) src = k0 + q * NW * LINES + line < k ? at + (int64_t)(q * NW * LINES) * step + off[0] : nullptr;
+      else src = k0 + line * 8u < k ? at + off[q] : nullptr;
+      to_lds(src ? src : reinterpret_cast<const char*>(&kZeros), lds + (q * NW + wave) * 1024u);
     }
   }
 };
@@ -196,29 +200,6 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-// Orders what stands since the last call: an LDS read after each matrix
-// instruction, then a share of the loads after each, so that the matrix cores
-// have work while the other queues fill.
-template <int READS, int LOADS, int MFMAS>
-__device__ __forceinline__ void mix() {
-  constexpr int PER = READS > MFMAS / 2 ? (READS * 2 + MFMAS - 1) / MFMAS : 1;   // reads before one
-  constexpr int FIRST = (READS + PER - 1) / PER, REST = MFMAS > FIRST ? MFMAS - FIRST : 0;
-#pragma unroll
-  for (int i = 0; i < FIRST; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // matrix instructions
-    __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);   // LDS reads
-  }
-  if constexpr (LOADS > 0 && REST > 0) {
-    constexpr int SHARE = (LOADS + REST - 1) / REST;
-#pragma unroll
-    for (int i = 0; i < REST; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, SHARE, 0);   // loads
-    }
-  }
-  __builtin_amdgcn_sched_barrier(0);
-}
-
 struct TileArgs {
   GemmArgs g;
   uint32_t tiles_n, tiles;  // tiles across, in all
@@ -245,7 +226,7 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
 template <typename T, int TM, int TN, int WM, int WN, int NS, bool A_ROWS_K, bool B_ROWS_K>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   constexpr int NW = WM * WN, MI = TM / WM / 32, NI = TN / WN / 32, BYTES = (TM + TN) * 128;
-  constexpr int LOADS = (TM + TN) / 8 / NW, READS = MI * (A_ROWS_K ? 2 : 1) + NI * (B_ROWS_K ? 2 : 1);
+  constexpr int LA = TM / 8 / NW, LOADS = LA + TN / 8 / NW;
   constexpr int PITCH = TN / WN + 4;
   static_assert(!A_ROWS_K || TM >= 64, "four 32-byte pieces to a line");
   static_assert(NW * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
@@ -273,61 +254,72 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 #pragma unroll
     for (int y = 0; y < NI; ++y) c[x][y] = f32x16(0.0f);
   typename Vec<T>::x8 fa[2][MI], fb[2][NI];
+  const uint32_t lds_at = lds_address(lds);
 
-  const auto load = [&](uint32_t s, bool whole) {
-    char* const buf = lds + (s % NS) * BYTES;
-    la.load(buf, k_first + s * kDepth, k_last, wave, whole);
-    lb.load(buf + TM * 128, k_first + s * kDepth, k_last, wave, whole);
+  const auto load_end = [&](uint32_t s) {
+    const uint32_t buf = lds_at + (s % NS) * BYTES;
+    la.load_end(buf, k_first + s * kDepth, k_last, wave);
+    lb.load_end(buf + TM * 128, k_first + s * kDepth, k_last, wave);
   };
-  const auto read = [&](uint32_t s, int kk, int to) {
-    const char* const buf = lds + (s % NS) * BYTES;
-#pragma unroll
-    for (int x = 0; x < MI; ++x) fa[to][x] = ra.read(buf, x, kk);
-#pragma unroll
-    for (int y = 0; y < NI; ++y) fb[to][y] = rb.read(buf + TM * 128, y, kk);
+  // A sixteenth of a step, in the order that stands here: the products of the
+  // fragments in `from`, and evenly between them the reads of sixteen kk of
+  // step `at` into the other set, and the loads of step `ahead`. A product
+  // waits only for its own fragments, which come in the order of their use.
+  const auto phase = [&](auto from_, uint32_t at, auto kk_, auto loads_, uint32_t ahead) {
+    constexpr int from = from_, kk = kk_, loads = loads_, M = MI * NI, F = MI + NI;
+    const char* const buf = lds + (at % NS) * BYTES;
+    const uint32_t to = lds_at + (ahead % NS) * BYTES, k0 = k_first + ahead * kDepth;
+    each<M>([&](auto i_) {
+      constexpr int i = i_, x = i / NI, y = i % NI;
+      c[x][y] = mfma32(fb[from][y], fa[from][x], c[x][y]);
+      each<(i + 1) * F / M - i * F / M>([&](auto f_) {
+        constexpr int f = i * F / M + f_;
+        if constexpr (f >= 1 && f <= NI) fb[from ^ 1][f - 1] = rb.read(buf + TM * 128, f - 1, kk);
+        else fa[from ^ 1][f ? f - NI : 0] = ra.read(buf, f ? f - NI : 0, kk);
+      });
+      each<(i + 1) * loads / M - i * loads / M>([&](auto l_) {
+        constexpr int l = i * loads / M + l_;
+        if constexpr (l < LA) la.load(to, k0, l, wave);
+        else lb.load(to + TM * 128, k0, l - LA, wave);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
-  const auto multiply = [&](int from) {
-#pragma unroll
-    for (int x = 0; x < MI; ++x)
-#pragma unroll
-      for (int y = 0; y < NI; ++y) c[x][y] = mfma32(fb[from][y], fa[from][x], c[x][y]);
-  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
 
   if (steps > 0) {
 #pragma unroll
     for (uint32_t s = 0; s < NS; ++s)
-      if (s < steps) load(s, false);
+      if (s < steps) load_end(s);
     if (steps >= NS) wait_and_meet<(NS - 1) * LOADS>();
     else wait_and_meet<0>();
-    read(0, 0, 0);
-    const auto three = [&](uint32_t s) {
+    fa[0][0] = ra.read(lds, 0, 0);
 #pragma unroll
-      for (int kk = 0; kk < 3; ++kk) {
-        read(s, kk + 1, (kk + 1) & 1);
-        multiply(kk & 1);
-        mix<READS, 0, MI * NI>();
-      }
-    };
+    for (int y = 0; y < NI; ++y) fb[0][y] = rb.read(lds + TM * 128, y, 0);
+#pragma unroll
+    for (int x = 1; x < MI; ++x) fa[0][x] = ra.read(lds, x, 0);
     // Where a step behaves as most do: more than the buffers hold ahead of
     // it, and the tiles that it loads are whole.
     const uint32_t whole = (k_last - k_first) / kDepth;
     uint32_t s = 0;
     for (; s + NS < whole; ++s) {
-      three(s);
+      phase(I0{}, s, I1{}, I0{}, s);
+      phase(I1{}, s, I2{}, I0{}, s);
+      phase(I0{}, s, I3{}, I0{}, s);
       // The next step's tiles are here, and no wave needs this one's again.
       wait_and_meet<(NS - 2) * LOADS>();
-      read(s + 1, 0, 0);
-      load(s + NS, true);
-      multiply(1);
-      mix<READS, LOADS, MI * NI>();
+      phase(I1{}, s + 1, I0{}, std::integral_constant<int, LOADS>{}, s + NS);
     }
     for (; s < steps; ++s) {
-      three(s);
+      phase(I0{}, s, I1{}, I0{}, s);
+      phase(I1{}, s, I2{}, I0{}, s);
+      phase(I0{}, s, I3{}, I0{}, s);
       wait_and_meet<0>();
-      if (s + NS < steps) load(s + NS, false);
-      read(s + 1 < steps ? s + 1 : s, 0, 0);   // the last step's is of no use, and in bounds
-      multiply(1);
-      mix<READS, 0, MI * NI>();
+      if (s + NS < steps) load_end(s + NS);
+      phase(I1{}, s + 1 < steps ? s + 1 : s, I0{}, I0{}, s);   // the last step's reads are of no use, and in bounds
     }
   }
   wait_and_meet<0>();   // no wave reads the buffers any more
