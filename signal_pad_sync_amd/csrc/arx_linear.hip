@@ -21,11 +21,11 @@ namespace {
 
 __host__ __device__ constexpr uint32_t cdiv(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 
-__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 template <int ACT>
@@ -149,34 +149,33 @@ struct Loader {
   }
 };
 
-// A fragment for the 32 x 32 x 16 matrix instruction: lane l holds row l % 32,
-// depths 8 (l / 32) + 0..7 of the kk-th sixteen.
+// A fragment for the 16 x 16 x 32 matrix instruction: lane l holds row l % 16,
+// depths 8 (l / 16) + 0..7 of the kk-th thirty-two.
 template <typename T, int TILE, bool ROWS_K>
 struct Fragments {
   typedef typename Vec<T>::x8 x8;
-  uint32_t at[ROWS_K ? 2 : 4];
+  uint32_t at[ROWS_K ? 4 : 2];
   // r0: the wave's first row, a multiple of 32, and of 64 where it has more than 32.
   __device__ __forceinline__ void init(uint32_t r0) {
     const uint32_t l = threadIdx.x & 63u;
     if constexpr (ROWS_K) {
       // A group of 16 lanes reads four depths of one 32-byte piece, 8 bytes a
       // lane, and gets each row's four depths.
-      const uint32_t j = l & 15u, depth = (l >> 5) * 8u + (j >> 2), piece = (l >> 4) & 1u;
+      const uint32_t j = l & 15u, depth = (l >> 4) * 8u + (j >> 2);
 #pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-        at[p] = depth * (TILE * 2u) + r0 / 64u * 128u + (((r0 / 16u + 2u * p + piece) & 3u) ^ (j >> 2)) * 32u +
-                (j & 3u) * 8u;
+      for (uint32_t p = 0; p < 4; ++p)
+        at[p] = depth * (TILE * 2u) + r0 / 64u * 128u + (((r0 / 16u + p) & 3u) ^ (j >> 2)) * 32u + (j & 3u) * 8u;
     } else {
 #pragma unroll
-      for (uint32_t kk = 0; kk < 4; ++kk) at[kk] = (r0 + (l & 31u)) * 128u + (((kk * 2u + (l >> 5)) ^ (l & 7u)) << 4);
+      for (uint32_t kk = 0; kk < 2; ++kk) at[kk] = (r0 + (l & 15u)) * 128u + (((kk * 4u + (l >> 4)) ^ (l & 7u)) << 4);
     }
   }
-  // The wave's rows [32 x, 32 x + 32), the kk-th sixteen depths.
+  // The wave's rows [16 x, 16 x + 16), the kk-th thirty-two depths.
   __device__ __forceinline__ x8 read(const char* lds, int x, int kk) const {
     if constexpr (ROWS_K) {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* P;
-      const char* const p = lds + at[x & 1] + (x >> 1) * 128 + kk * (16 * TILE * 2);
+      const char* const p = lds + at[x & 3] + (x >> 2) * 128 + kk * (32 * TILE * 2);
       union {
         s16x4 half[2];
         x8 all;
@@ -185,7 +184,7 @@ struct Fragments {
       u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 4 * TILE * 2));
       return u.all;
     } else {
-      return *reinterpret_cast<const x8*>(lds + at[kk] + x * 4096);
+      return *reinterpret_cast<const x8*>(lds + at[kk] + x * 2048);
     }
   }
 };
@@ -219,13 +218,15 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
   *tj = in / high;
 }
 
-// C's TM x TN tile on WM x WN waves, each in 32 x 32 blocks.
-// The depth runs through NS buffers: while the matrix cores work on one, the
-// loads of the next NS - 1 are under way. B's fragments take the matrix
-// instruction's rows, so a lane's sums are neighbours in a row of C.
+// C's TM x TN tile on WM x WN waves, each in 16 x 16 blocks. The depth runs
+// through NS buffers: while the matrix cores work on one, the loads of the
+// next NS - 1 are under way. B's fragments take the matrix instruction's rows,
+// so a lane's sums are neighbours in a row of C. The 16 x 16 x 32 instruction
+// moves a fifth less through the registers for a product than 32 x 32 x 16,
+// and where power bounds the clock that is time.
 template <typename T, int TM, int TN, int WM, int WN, int NS, bool A_ROWS_K, bool B_ROWS_K>
 __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
-  constexpr int NW = WM * WN, MI = TM / WM / 32, NI = TN / WN / 32, BYTES = (TM + TN) * 128;
+  constexpr int NW = WM * WN, MI = TM / WM / 16, NI = TN / WN / 16, BYTES = (TM + TN) * 128;
   constexpr int LA = TM / 8 / NW, LOADS = LA + TN / 8 / NW;
   constexpr int PITCH = TN / WN + 4;
   static_assert(!A_ROWS_K || TM >= 64, "four 32-byte pieces to a line");
@@ -248,11 +249,11 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   Fragments<T, TN, B_ROWS_K> rb;
   ra.init(wi);
   rb.init(wj);
-  f32x16 c[MI][NI];
+  f32x4 c[MI][NI];
 #pragma unroll
   for (int x = 0; x < MI; ++x)
 #pragma unroll
-    for (int y = 0; y < NI; ++y) c[x][y] = f32x16(0.0f);
+    for (int y = 0; y < NI; ++y) c[x][y] = f32x4(0.0f);
   typename Vec<T>::x8 fa[2][MI], fb[2][NI];
   const uint32_t lds_at = lds_address(lds);
 
@@ -261,34 +262,36 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
     la.load_end(buf, k_first + s * kDepth, k_last, wave);
     lb.load_end(buf + TM * 128, k_first + s * kDepth, k_last, wave);
   };
-  // A sixteenth of a step, in the order that stands here: the products of the
-  // fragments in `from`, and evenly between them the reads of sixteen kk of
-  // step `at` into the other set, and the loads of step `ahead`. A product
-  // waits only for its own fragments, which come in the order of their use.
+  // Half a step, in the order that stands here: the products of the fragments
+  // in `from`; between them, over three quarters of the time, the reads of the
+  // kk-th half of step `at` into the other set, and evenly the loads of step
+  // `ahead`. A product waits only for its own fragments, which come in the
+  // order of their use.
   const auto phase = [&](auto from_, uint32_t at, auto kk_, auto loads_, uint32_t ahead) {
-    constexpr int from = from_, kk = kk_, loads = loads_, M = MI * NI, F = MI + NI;
+    constexpr int from = from_, kk = kk_, loads = loads_, M = MI * NI, F = MI + NI, SPAN = M * 3 / 4;
     const char* const buf = lds + (at % NS) * BYTES;
     const uint32_t to = lds_at + (ahead % NS) * BYTES, k0 = k_first + ahead * kDepth;
     each<M>([&](auto i_) {
       constexpr int i = i_, x = i / NI, y = i % NI;
-      c[x][y] = mfma32(fb[from][y], fa[from][x], c[x][y]);
-      each<(i + 1) * F / M - i * F / M>([&](auto f_) {
-        constexpr int f = i * F / M + f_;
+      constexpr int f0 = i >= SPAN ? F : i * F / SPAN, f1 = i + 1 >= SPAN ? F : (i + 1) * F / SPAN;
+      constexpr int l0 = i * loads / M, l1 = (i + 1) * loads / M;
+      c[x][y] = mfma(fb[from][y], fa[from][x], c[x][y]);
+      each<f1 - f0>([&](auto f_) {
+        constexpr int f = f0 + f_;
         if constexpr (f >= 1 && f <= NI) fb[from ^ 1][f - 1] = rb.read(buf + TM * 128, f - 1, kk);
         else fa[from ^ 1][f ? f - NI : 0] = ra.read(buf, f ? f - NI : 0, kk);
       });
-      each<(i + 1) * loads / M - i * loads / M>([&](auto l_) {
-        constexpr int l = i * loads / M + l_;
+      each<l1 - l0>([&](auto l_) {
+        constexpr int l = l0 + l_;
         if constexpr (l < LA) la.load(to, k0, l, wave);
         else lb.load(to + TM * 128, k0, l - LA, wave);
       });
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (f1 > f0 || l1 > l0) __builtin_amdgcn_sched_barrier(0);
     });
+    __builtin_amdgcn_sched_barrier(0);
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
 
   if (steps > 0) {
 #pragma unroll
@@ -307,16 +310,12 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
     uint32_t s = 0;
     for (; s + NS < whole; ++s) {
       phase(I0{}, s, I1{}, I0{}, s);
-      phase(I1{}, s, I2{}, I0{}, s);
-      phase(I0{}, s, I3{}, I0{}, s);
       // The next step's tiles are here, and no wave needs this one's again.
       wait_and_meet<(NS - 2) * LOADS>();
       phase(I1{}, s + 1, I0{}, std::integral_constant<int, LOADS>{}, s + NS);
     }
     for (; s < steps; ++s) {
       phase(I0{}, s, I1{}, I0{}, s);
-      phase(I1{}, s, I2{}, I0{}, s);
-      phase(I0{}, s, I3{}, I0{}, s);
       wait_and_meet<0>();
       if (s + NS < steps) load_end(s + NS);
       phase(I1{}, s + 1 < steps ? s + 1 : s, I0{}, I0{}, s);   // the last step's reads are of no use, and in bounds
@@ -329,15 +328,13 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   float* const turn = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
   float* const partial = t.partial ? t.partial + (size_t)blockIdx.y * g.m * g.n : nullptr;
   constexpr int ACROSS = TN / WN / 8;   // lanes across the wave's columns, eight each
-  each<MI>([&](auto at) {
+  each<MI / 2>([&](auto at) {
     constexpr int x = at;
 #pragma unroll
-    for (int y = 0; y < NI; ++y)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 v = {c[x][y][4 * q], c[x][y][4 * q + 1], c[x][y][4 * q + 2], c[x][y][4 * q + 3]};
-        *reinterpret_cast<f32x4*>(turn + (lane & 31u) * PITCH + y * 32 + q * 8 + (lane >> 5) * 4u) = v;
-      }
+      for (int y = 0; y < NI; ++y)
+        *reinterpret_cast<f32x4*>(turn + (h * 16 + (lane & 15u)) * PITCH + y * 16 + (lane >> 4) * 4u) = c[2 * x + h][y];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 2
     for (int e = 0; e < 32 * ACROSS / 64; ++e) {
@@ -360,13 +357,6 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 }
 
 // ---- a few rows -------------------------------------------------------------
-
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 
 // Up to 16 MT rows of A against ROWS rows of B a workgroup (8: the matrix
 // instruction's other rows repeat them), both with the depth
@@ -411,7 +401,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) c[t] = mfma16(fb[u][h], fa[u][t][h], c[t]);
+        for (int h = 0; h < 2; ++h) c[t] = mfma(fb[u][h], fa[u][t][h], c[t]);
   }
   for (; s * 64u < k_end; s += WAVES) {
 #pragma unroll
@@ -420,7 +410,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
       const int valid = k < k_end ? (int)min(8u, k_end - k) : 0;
       const x8 fb = load8(b + s * 64u + h * 32, valid);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) c[t] = mfma16(fb, load8(a[t] + s * 64u + h * 32, valid), c[t]);
+      for (int t = 0; t < MT; ++t) c[t] = mfma(fb, load8(a[t] + s * 64u + h * 32, valid), c[t]);
     }
   }
 #pragma unroll
