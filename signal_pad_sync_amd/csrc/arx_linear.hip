@@ -257,10 +257,17 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   typename Vec<T>::x8 fa[2][MI], fb[2][NI];
   const uint32_t lds_at = lds_address(lds);
 
+  // Depth of step s. Rows a power of two apart put one depth of all of them on
+  // few memory channels, so the XCDs start at different depths and go round.
+  const uint32_t whole = (k_last - k_first) / kDepth, start = whole / 8u * (blockIdx.x & 7u);
+  const auto depth_of = [&](uint32_t s) {
+    const uint32_t turned = s + start < whole ? s + start : s + start - whole;
+    return k_first + (s < whole ? turned : s) * kDepth;
+  };
   const auto load_end = [&](uint32_t s) {
-    const uint32_t buf = lds_at + (s % NS) * BYTES;
-    la.load_end(buf, k_first + s * kDepth, k_last, wave);
-    lb.load_end(buf + TM * 128, k_first + s * kDepth, k_last, wave);
+    const uint32_t buf = lds_at + (s % NS) * BYTES, k0 = depth_of(s);
+    la.load_end(buf, k0, k_last, wave);
+    lb.load_end(buf + TM * 128, k0, k_last, wave);
   };
   // Half a step, in the order that stands here: the products of the fragments
   // in `from`; between them, over three quarters of the time, the reads of the
@@ -270,7 +277,7 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   const auto phase = [&](auto from_, uint32_t at, auto kk_, auto loads_, uint32_t ahead) {
     constexpr int from = from_, kk = kk_, loads = loads_, M = MI * NI, F = MI + NI, SPAN = M * 3 / 4;
     const char* const buf = lds + (at % NS) * BYTES;
-    const uint32_t to = lds_at + (ahead % NS) * BYTES, k0 = k_first + ahead * kDepth;
+    const uint32_t to = lds_at + (ahead % NS) * BYTES, k0 = depth_of(ahead);
     each<M>([&](auto i_) {
       constexpr int i = i_, x = i / NI, y = i % NI;
       constexpr int f0 = i >= SPAN ? F : i * F / SPAN, f1 = i + 1 >= SPAN ? F : (i + 1) * F / SPAN;
@@ -306,7 +313,6 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
     for (int x = 1; x < MI; ++x) fa[0][x] = ra.read(lds, x, 0);
     // Where a step behaves as most do: more than the buffers hold ahead of
     // it, and the tiles that it loads are whole.
-    const uint32_t whole = (k_last - k_first) / kDepth;
     uint32_t s = 0;
     for (; s + NS < whole; ++s) {
       phase(I0{}, s, I1{}, I0{}, s);
