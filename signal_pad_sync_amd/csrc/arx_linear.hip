@@ -229,7 +229,6 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   constexpr int NW = WM * WN, MI = TM / WM / 16, NI = TN / WN / 16, BYTES = (TM + TN) * 128;
   constexpr int LA = TM / 8 / NW, LOADS = LA + TN / 8 / NW;
   constexpr int PITCH = TN / WN + 4;
-  static_assert(!A_ROWS_K || TM >= 64, "four 32-byte pieces to a line");
   static_assert(NW * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
   static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
   __shared__ __align__(1024) char lds[NS * BYTES];
@@ -364,33 +363,26 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
 
 // ---- a few rows -------------------------------------------------------------
 
-// Up to 16 MT rows of A against ROWS rows of B a workgroup (8: the matrix
-// instruction's other rows repeat them), both with the depth
+// Up to 16 rows of A against 16 rows of B a workgroup, both with the depth
 // contiguous and at any alignment. Bound by reading B once: it goes straight
 // to registers, and the sixteen waves take the depth's 64-deep chunks in turn,
 // so that a workgroup has all of a common depth under way at once; their sums
 // meet in shared memory. Four lanes read 64 consecutive bytes of a row.
-template <typename T, int MT, int ROWS>
-__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs ta) {
-  const GemmArgs& g = ta.g;
-  constexpr int WAVES = 16, UNROLL = MT == 4 ? 2 : 4, PITCH = 20;
+template <typename T>
+__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs t) {
+  const GemmArgs& g = t.g;
+  constexpr int WAVES = 16, UNROLL = 4, PITCH = 20;
   typedef typename Vec<T>::x8 x8;
-  __shared__ __align__(16) float lds[WAVES][MT * 16][PITCH];
+  __shared__ __align__(16) float lds[WAVES][16][PITCH];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 8u;
-  const uint32_t j0 = blockIdx.x * ROWS;
-  const uint32_t k_first = blockIdx.y * ta.depth, k_end = min(g.k, k_first + ta.depth);
-  const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r % ROWS, g.n - 1u) * g.ldb + k_lane;
-  const T* a[MT];
-  f32x4 c[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    a[t] = static_cast<const T*>(g.a) + (int64_t)min(t * 16u + r, g.m - 1u) * g.lda + k_lane;
-    c[t] = f32x4(0.0f);
-  }
-  const uint32_t whole = k_end / 64u;
+  const uint32_t j0 = blockIdx.x * 16u;
+  const uint32_t k_first = blockIdx.y * t.depth, k_end = min(g.k, k_first + t.depth);
+  const T* const a = static_cast<const T*>(g.a) + (int64_t)min(r, g.m - 1u) * g.lda + k_lane;
+  const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r, g.n - 1u) * g.ldb + k_lane;
+  f32x4 c = f32x4(0.0f);
   uint32_t s = k_first / 64u + wave;
-  for (; s + (UNROLL - 1) * WAVES < whole; s += UNROLL * WAVES) {
-    x8 fb[UNROLL][2], fa[UNROLL][MT][2];
+  for (; s + (UNROLL - 1) * WAVES < k_end / 64u; s += UNROLL * WAVES) {
+    x8 fb[UNROLL][2], fa[UNROLL][2];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
@@ -398,32 +390,25 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) fa[u][t][h] = load8(a[t] + (s + u * WAVES) * 64u + h * 32, 8);
+      for (int h = 0; h < 2; ++h) fa[u][h] = load8(a + (s + u * WAVES) * 64u + h * 32, 8);
     __builtin_amdgcn_sched_barrier(0);   // every load is under way before the first product waits
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) c[t] = mfma(fb[u][h], fa[u][t][h], c[t]);
+      for (int h = 0; h < 2; ++h) c = mfma(fb[u][h], fa[u][h], c);
   }
   for (; s * 64u < k_end; s += WAVES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t k = s * 64u + h * 32u + k_lane;
       const int valid = k < k_end ? (int)min(8u, k_end - k) : 0;
-      const x8 fb = load8(b + s * 64u + h * 32, valid);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) c[t] = mfma(fb, load8(a[t] + s * 64u + h * 32, valid), c[t]);
+      c = mfma(load8(b + s * 64u + h * 32, valid), load8(a + s * 64u + h * 32, valid), c);
     }
   }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4*>(&lds[wave][t * 16 + r][(lane >> 4) * 4u]) = c[t];
+  *reinterpret_cast<f32x4*>(&lds[wave][r][(lane >> 4) * 4u]) = c;
   __syncthreads();
-  const uint32_t i = threadIdx.x / (ROWS / 8), j = threadIdx.x % (ROWS / 8) * 8u;
-  if (i >= MT * 16) return;
+  const uint32_t i = threadIdx.x / 2u, j = threadIdx.x % 2u * 8u;
+  if (i >= 16u) return;
   f32x8 v = f32x8(0.0f);
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
@@ -434,9 +419,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
       v[e + 4] += hi[e];
     }
   }
-  if (!ta.partial) epilogue8<T>(g, i, j0 + j, v);
+  if (!t.partial) epilogue8<T>(g, i, j0 + j, v);
   else if (i < g.m && j0 + j < g.n)
-    store8<float>(ta.partial + ((size_t)blockIdx.y * g.m + i) * g.n + j0 + j, v,
+    store8<float>(t.partial + ((size_t)blockIdx.y * g.m + i) * g.n + j0 + j, v,
                   g.n - j0 - j < 8u ? (int)(g.n - j0 - j) : 8);
 }
 
@@ -449,6 +434,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* part
     const uint32_t i = (uint32_t)(e / across), j = (uint32_t)(e % across) * 8u;
     const int valid = g.n - j < 8u ? (int)(g.n - j) : 8;
     f32x8 c = load8(partial + (size_t)i * g.n + j, valid);
+#pragma unroll 4
     for (int s = 1; s < splits; ++s) c += load8(partial + ((size_t)s * g.m + i) * g.n + j, valid);
     epilogue8<T>(g, i, j, c);
   }
@@ -481,7 +467,7 @@ bool loads_as_is(const void* p, int64_t ld, uint32_t contiguous) {
 size_t padded_bytes(uint32_t rows, uint32_t cols) { return ((size_t)rows * (cdiv(cols, 8) * 8u) * 2u + 255) & ~(size_t)255; }
 
 // How a product is cut: the kernel, and workgroups along the depth.
-enum Cut { ROWS8, ROWS16, T32x128, T64x64, T64x128, T128x128, T256x256, CUTS };
+enum Cut { ROWS16, T64x64, T64x128, T128x128, T256x256, CUTS };
 struct Shape {
   int cut;
   uint32_t splits;
@@ -490,21 +476,51 @@ struct Shape {
 
 constexpr uint32_t kCus = 256;
 
+// What a cut costs, in microseconds: a launch, a 64-deep step of a workgroup
+// that waits for its loads, the same step where the CU is kept busy, and a
+// workgroup's start and end; `resident` workgroups share a CU. A split product
+// pays for its partial sums and their joining. The numbers are a least-squares
+// fit to the times of 1100 cuts of 240 products (1 to 8192 rows, widths and
+// depths of 256 to 8192, the three layouts) on an MI355X; the cut with the
+// least cost by them is on average 1.5 % slower than the fastest one measured.
+struct CutCost {
+  float launch, wait, busy, group;
+  uint32_t tm, tn, resident;
+};
+constexpr CutCost kCost[CUTS] = {{1.4f, 0.112f, 0.115f, 2.0f, 16, 16, 1},
+                                 {3.1f, 0.264f, 0.202f, 1.0f, 64, 64, 2},
+                                 {3.2f, 0.437f, 0.329f, 1.6f, 64, 128, 2},
+                                 {3.4f, 0.657f, 0.498f, 2.4f, 128, 128, 2},
+                                 {0.0f, 1.224f, 1.242f, 11.2f, 256, 256, 1}};
+constexpr float kJoin = 1.7f, kJoinSplit = 0.24f, kJoinBytes = 0.25e-6f;
+
 Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
-  Shape s;
-  const uint64_t big = (uint64_t)cdiv(m, 256) * cdiv(n, 256), mid = (uint64_t)cdiv(m, 128) * cdiv(n, 128);
-  s.cut = big >= kCus ? T256x256 : mid >= kCus / 2 ? T128x128 : T64x64;
-  s.splits = 1;
-  uint64_t tiles = s.cut == T256x256 ? big : s.cut == T128x128 ? mid : (uint64_t)cdiv(m, 64) * cdiv(n, 64);
-  if (m <= 16 && !a_rows_k && !b_rows_k) s.cut = ROWS16, tiles = kCus;
-  if (tiles < kCus && k >= 1024) {
-    uint32_t want = (uint32_t)(2 * kCus / tiles), most = k / 512;
-    if (want > most) want = most;
-    if (want > 1) s.splits = want;
+  const uint32_t steps = cdiv(k ? k : 1, kDepth);
+  Shape best{T64x64, 1, steps * kDepth};
+  float least = 0.0f;
+  // B streams past once for up to 16 rows of A: 9.7 us against 11.9 in tiles
+  // at 1 x 4096 x 4096, 12.2 against 12.7 at 16 rows, 24 rows 13.9 against 12.8.
+  const bool rows = m <= 16 && !a_rows_k && !b_rows_k;
+  for (int c = rows ? ROWS16 : T64x64; c < (rows ? T64x64 : CUTS); ++c) {
+    const CutCost& t = kCost[c];
+    const uint64_t tiles = (uint64_t)cdiv(m, t.tm) * cdiv(n, t.tn);
+    for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u}) {
+      // no split under 128 deep, nor where the CUs are taken as it is; half of
+      // them draw all that memory gives to B's rows
+      if (s > 1 && (steps < 2 * s || tiles * s > (c == ROWS16 ? kCus / 2 : 4 * kCus))) break;
+      const uint32_t depth = cdiv(steps, s), splits = cdiv(steps, depth);
+      const float per_cu = (float)((tiles * splits + kCus - 1) / kCus);
+      const float turns = (float)((uint32_t)(per_cu + t.resident - 1) / t.resident);
+      const float waiting = t.wait * turns, busy = t.busy * per_cu;
+      float cost = t.launch + (float)depth * (waiting > busy ? waiting : busy) + t.group * per_cu;
+      if (splits > 1) cost += kJoin + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
+      if (least == 0.0f || cost < least) {
+        least = cost;
+        best = {c, splits, depth * kDepth};
+      }
+    }
   }
-  s.depth = cdiv(cdiv(k ? k : 1, s.splits), kDepth) * kDepth;
-  s.splits = cdiv(k ? k : 1, s.depth);
-  return s;
+  return best;
 }
 
 template <typename T, int TM, int TN, int WM, int WN, int NS>
@@ -515,13 +531,13 @@ hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
   const dim3 grid(t.tiles, splits);
   if (!g.a_rows_k && !g.b_rows_k) tile_kernel<T, TM, TN, WM, WN, NS, false, false><<<grid, WM * WN * 64, 0, stream>>>(t);
   else if (!g.a_rows_k) tile_kernel<T, TM, TN, WM, WN, NS, false, true><<<grid, WM * WN * 64, 0, stream>>>(t);
-  else if constexpr (TM >= 64) tile_kernel<T, TM, TN, WM, WN, NS, true, true><<<grid, WM * WN * 64, 0, stream>>>(t);
+  else tile_kernel<T, TM, TN, WM, WN, NS, true, true><<<grid, WM * WN * 64, 0, stream>>>(t);
   return hipGetLastError();
 }
 
-template <typename T, int ROWS>
+template <typename T>
 hipError_t launch_rows(const TileArgs& t, uint32_t splits, hipStream_t stream) {
-  rows_kernel<T, 1, ROWS><<<dim3(cdiv(t.g.n, ROWS), splits), 1024, 0, stream>>>(t);
+  rows_kernel<T><<<dim3(cdiv(t.g.n, 16), splits), 1024, 0, stream>>>(t);
   return hipGetLastError();
 }
 
@@ -551,9 +567,7 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   t.depth = s.depth;
   t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;
   switch (s.cut) {
-    case ROWS8: rc = launch_rows<T, 8>(t, s.splits, stream); break;
-    case ROWS16: rc = launch_rows<T, 16>(t, s.splits, stream); break;
-    case T32x128: rc = launch_tiles<T, 32, 128, 1, 4, 4>(t, s.splits, stream); break;
+    case ROWS16: rc = launch_rows<T>(t, s.splits, stream); break;
     case T64x64: rc = launch_tiles<T, 64, 64, 2, 2, 4>(t, s.splits, stream); break;
     case T64x128: rc = launch_tiles<T, 64, 128, 2, 2, 3>(t, s.splits, stream); break;
     case T128x128: rc = launch_tiles<T, 128, 128, 2, 2, 2>(t, s.splits, stream); break;
