@@ -54,15 +54,22 @@ __device__ __forceinline__ void each(F f) {
   each_of(std::make_integer_sequence<int, N>{}, f);
 }
 
-// Eight sums of row i, columns j.. : bias, z, activation, residual, y.
+// Eight sums of row i, columns j.. : bias, z, activation, residual, y. The
+// residual comes as an argument, so that it can be asked for ahead of time.
 template <typename T>
-__device__ __forceinline__ void epilogue8(const GemmArgs& g, uint32_t i, uint32_t j, f32x8 c) {
+__device__ __forceinline__ typename Vec<T>::x8 residual8(const GemmArgs& g, uint32_t i, uint32_t j) {
+  const int valid = i < g.m && j < g.n ? (int)min(8u, g.n - j) : 0;
+  return load8(static_cast<const T*>(g.residual.p) + (int64_t)i * g.residual.ld + j, g.residual.p ? valid : 0);
+}
+template <typename T>
+__device__ __forceinline__ void epilogue8(const GemmArgs& g, uint32_t i, uint32_t j, f32x8 c,
+                                          typename Vec<T>::x8 residual) {
   if (i >= g.m || j >= g.n) return;
   const int valid = g.n - j < 8u ? (int)(g.n - j) : 8;
   if (g.bias) c += widen(load8(static_cast<const T*>(g.bias) + j, valid));
   if (g.z.p) store8<T>(static_cast<T*>(g.z.p) + (int64_t)i * g.z.ld + j, narrow<T>(c), valid);
   act8(g.act, c);
-  if (g.residual.p) c += widen(load8(static_cast<const T*>(g.residual.p) + (int64_t)i * g.residual.ld + j, valid));
+  if (g.residual.p) c += widen(residual);
   store8<T>(static_cast<T*>(g.y.p) + (int64_t)i * g.y.ld + j, narrow<T>(c), valid);
 }
 
@@ -333,27 +340,34 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   float* const turn = reinterpret_cast<float*>(lds) + wave * (32 * PITCH);
   float* const partial = t.partial ? t.partial + (size_t)blockIdx.y * g.m * g.n : nullptr;
   constexpr int ACROSS = TN / WN / 8;   // lanes across the wave's columns, eight each
+  constexpr int EACH = 32 * ACROSS / 64, DOWN = 64 / ACROSS;   // rows of a lane, rows of a wave at a time
+  const uint32_t row = lane / ACROSS, col = lane % ACROSS * 8u, j = j0 + wj + col;
   each<MI / 2>([&](auto at) {
     constexpr int x = at;
+    const uint32_t first = i0 + wi + x * 32u + row;
+    typename Vec<T>::x8 residual[EACH];
+    if (!partial) {
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) residual[e] = residual8<T>(g, first + e * DOWN, j);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int y = 0; y < NI; ++y)
         *reinterpret_cast<f32x4*>(turn + (h * 16 + (lane & 15u)) * PITCH + y * 16 + (lane >> 4) * 4u) = c[2 * x + h][y];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll 2
-    for (int e = 0; e < 32 * ACROSS / 64; ++e) {
-      const uint32_t r = e * (64 / ACROSS) + lane / ACROSS, col = lane % ACROSS * 8u;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+      const uint32_t i = first + e * DOWN;
       f32x8 v;
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + r * PITCH + col);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + r * PITCH + col + 4);
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + (row + e * DOWN) * PITCH + col);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + (row + e * DOWN) * PITCH + col + 4);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         v[n] = lo[n];
         v[n + 4] = hi[n];
       }
-      const uint32_t i = i0 + wi + x * 32u + r, j = j0 + wj + col;
-      if (!partial) epilogue8<T>(g, i, j, v);
+      if (!partial) epilogue8<T>(g, i, j, v, residual[e]);
       else if (i < g.m && j < g.n)
         store8<float>(partial + (size_t)i * g.n + j, v, g.n - j < 8u ? (int)(g.n - j) : 8);
     }
@@ -419,7 +433,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
       v[e + 4] += hi[e];
     }
   }
-  if (!t.partial) epilogue8<T>(g, i, j0 + j, v);
+  if (!t.partial) epilogue8<T>(g, i, j0 + j, v, residual8<T>(g, i, j0 + j));
   else if (i < g.m && j0 + j < g.n)
     store8<float>(t.partial + ((size_t)blockIdx.y * g.m + i) * g.n + j0 + j, v,
                   g.n - j0 - j < 8u ? (int)(g.n - j0 - j) : 8);
@@ -436,18 +450,28 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* part
     f32x8 c = load8(partial + (size_t)i * g.n + j, valid);
 #pragma unroll 4
     for (int s = 1; s < splits; ++s) c += load8(partial + ((size_t)s * g.m + i) * g.n + j, valid);
-    epilogue8<T>(g, i, j, c);
+    epilogue8<T>(g, i, j, c, residual8<T>(g, i, j));
   }
 }
 
-// Rows copied to a row distance that is a multiple of eight, zero past their end.
+// Lines copied to a distance that is a multiple of eight, zero past their end:
+// up to two operands in one launch.
+struct PadArgs {
+  const void* p[2];
+  int64_t ld[2];
+  void* out[2];
+  uint32_t cols[2];
+  uint64_t items[2];   // groups of eight in all
+};
 template <typename T>
-__global__ __launch_bounds__(256) void pad_kernel(const T* p, int64_t ld, T* out, uint32_t rows, uint32_t cols) {
-  const uint32_t across = cdiv(cols, 8);
-  const uint64_t all = (uint64_t)rows * across, step = (uint64_t)gridDim.x * 256u;
-  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < all; e += step) {
-    const uint32_t r = (uint32_t)(e / across), j = (uint32_t)(e % across) * 8u;
-    store8<T>(out + e * 8u, load8(p + (int64_t)r * ld + j, cols - j < 8u ? (int)(cols - j) : 8), 8);
+__global__ __launch_bounds__(256) void pad_kernel(PadArgs a) {
+  const uint64_t step = (uint64_t)gridDim.x * 256u;
+  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < a.items[0] + a.items[1]; e += step) {
+    const int w = e < a.items[0] ? 0 : 1;
+    const uint64_t item = w ? e - a.items[0] : e;
+    const uint32_t cols = a.cols[w], across = cdiv(cols, 8), j = (uint32_t)(item % across) * 8u;
+    const T* const from = static_cast<const T*>(a.p[w]) + (int64_t)(item / across) * a.ld[w] + j;
+    store8<T>(static_cast<T*>(a.out[w]) + item * 8u, load8(from, cols - j < 8u ? (int)(cols - j) : 8), 8);
   }
 }
 
@@ -549,20 +573,26 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   const Shape s = shape_of(g.m, g.n, g.k, g.a_rows_k, g.b_rows_k);
   hipError_t rc = hipSuccess;
   char* space = static_cast<char*>(g.workspace);
-  const auto as_is = [&](const void** p, int64_t* ld, bool rows_k, uint32_t rows, bool whole) {
-    const uint32_t lines = rows_k ? g.k : rows, contiguous = rows_k ? rows : g.k;
-    if (g.k == 0 || loads_as_is(*p, *ld, whole ? 0 : contiguous)) return hipSuccess;
-    const uint32_t across = cdiv(contiguous, 8);
-    pad_kernel<T><<<grid_of((uint64_t)lines * across), 256, 0, stream>>>(
-        static_cast<const T*>(*p), *ld, reinterpret_cast<T*>(space), lines, contiguous);
-    *p = space;
-    *ld = (int64_t)across * 8;
-    space += padded_bytes(lines, contiguous);
-    return hipGetLastError();
-  };
-  if (s.cut > ROWS16) {   // the tiles' loads go by whole chunks
-    if ((rc = as_is(&g.a, &g.lda, g.a_rows_k, g.m, g.a_whole)) != hipSuccess) return rc;
-    if ((rc = as_is(&g.b, &g.ldb, g.b_rows_k, g.n, false)) != hipSuccess) return rc;
+  if (s.cut != ROWS16 && g.k > 0) {   // the tiles' loads go by whole chunks
+    PadArgs pad{};
+    const auto as_is = [&](int w, const void** p, int64_t* ld, bool rows_k, uint32_t rows, bool whole) {
+      const uint32_t lines = rows_k ? g.k : rows, contiguous = rows_k ? rows : g.k;
+      if (loads_as_is(*p, *ld, whole ? 0 : contiguous)) return;
+      pad.p[w] = *p;
+      pad.ld[w] = *ld;
+      pad.out[w] = space;
+      pad.cols[w] = contiguous;
+      pad.items[w] = (uint64_t)lines * cdiv(contiguous, 8);
+      *p = space;
+      *ld = (int64_t)cdiv(contiguous, 8) * 8;
+      space += padded_bytes(lines, contiguous);
+    };
+    as_is(0, &g.a, &g.lda, g.a_rows_k, g.m, g.a_whole);
+    as_is(1, &g.b, &g.ldb, g.b_rows_k, g.n, false);
+    if (pad.items[0] + pad.items[1] > 0) {
+      pad_kernel<T><<<grid_of(pad.items[0] + pad.items[1]), 256, 0, stream>>>(pad);
+      if ((rc = hipGetLastError()) != hipSuccess) return rc;
+    }
   }
   t.depth = s.depth;
   t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;

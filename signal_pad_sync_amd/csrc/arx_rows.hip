@@ -202,23 +202,42 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
 #pragma unroll
     for (int k = 0; k < SUMS; ++k) sum[k][i] = f32x8(0.0f);
   }
-  int turn = 0;
-  for (uint64_t base = (uint64_t)blockIdx.x * R; base < a.rows; base += (uint64_t)gridDim.x * R, turn ^= 1) {
-    const bool live = base + team < a.rows;
-    const uint32_t r = live ? (uint32_t)base + team : 0u;
-    const float mean = live ? a.mean[r] : 0.0f, rstd = live ? a.rstd[r] : 0.0f;
-    f32x8 dy[V], xh[V];
-    float s1 = 0.0f, s2 = 0.0f;
+  // A row's values are asked for while the row before is worked on.
+  typedef typename Vec<T>::x8 x8;
+  x8 in_dy[V], in_x[V], in_dh[V];
+  float in_mean = 0.0f, in_rstd = 0.0f;
+  const auto ask = [&](uint64_t row) {
+    const bool live = row < a.rows;
+    const uint32_t r = live ? (uint32_t)row : 0u;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t g = lane + i * L;
       const int valid = live ? valid_of(g, a.cols) : 0;
-      dy[i] = widen(load8(row_of<T>(a.dy, r) + g * 8u, valid));
-      xh[i] = widen(load8(row_of<T>(a.x, r) + g * 8u, valid));
+      in_dy[i] = load8(row_of<T>(a.dy, r) + g * 8u, valid);
+      in_x[i] = load8(row_of<T>(a.x, r) + g * 8u, valid);
+      if (JOIN) in_dh[i] = load8(row_of<T>(a.dh, r) + g * 8u, a.dh.p ? valid : 0);
     }
+    in_mean = live ? a.mean[r] : 0.0f;
+    in_rstd = live ? a.rstd[r] : 0.0f;
+  };
+  int turn = 0;
+  const uint64_t stride = (uint64_t)gridDim.x * R;
+  ask((uint64_t)blockIdx.x * R + team);
+  for (uint64_t base = (uint64_t)blockIdx.x * R; base < a.rows; base += stride, turn ^= 1) {
+    const bool live = base + team < a.rows;
+    const uint32_t r = live ? (uint32_t)base + team : 0u;
+    const float mean = in_mean, rstd = in_rstd;
+    f32x8 dy[V], xh[V], dh[V];
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xh[i] = centred(xh[i], mean, live ? valid_of(lane + i * L, a.cols) : 0) * rstd;
+      dy[i] = widen(in_dy[i]);
+      xh[i] = centred(widen(in_x[i]), mean, live ? valid_of(lane + i * L, a.cols) : 0) * rstd;
+      if (JOIN) dh[i] = widen(in_dh[i]);
+    }
+    if (base + stride < a.rows) ask(base + stride + team);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
       const f32x8 g = dy[i] * w[i];
       s1 += sum8(g);
       s2 += sum8(g * xh[i]);
@@ -248,7 +267,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
       sum[0][i] += dy[i] * xh[i];
       sum[1][i] += dy[i];
       if constexpr (JOIN) {
-        if (a.dh.p) d += widen(load8(row_of<T>(a.dh, r) + g * 8u, valid));
+        if (a.dh.p) d += dh[i];
         if (a.dresidual.p) store8<T>(row_of<T>(a.dresidual, r) + g * 8u, narrow<T>(d), valid);
         if (valid > 0) d = drop8(d, (uint64_t)r * groups + g, a.drop);
         if (valid > 0) sum[2][i] += d;
@@ -469,8 +488,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSumArgs a) {
   if (!a.out[k]) return;
   const uint32_t lane = threadIdx.x & 63u, slice = threadIdx.x >> 6, c = blockIdx.x * 64u + lane;
   float s = 0.0f;
-  if (c < a.cols)
+  if (c < a.cols) {
+#pragma unroll 8
     for (uint32_t g = slice; g < a.groups; g += 16u) s += a.partial[((size_t)g * a.sums + k) * a.cols + c];
+  }
   lds[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || c >= a.cols) return;
@@ -493,11 +514,16 @@ struct ColumnShape {
 ColumnShape column_shape(uint32_t rows, uint32_t cols, bool sums) {
   const uint32_t groups = cdiv(cols, 8);
   ColumnShape s;
-  s.lg = 0;
-  while (s.lg < 8 && (1u << s.lg) < groups) ++s.lg;
+  // As many lanes across as leave at most an eighth of them idle, at least 16
+  // (256 consecutive bytes of a 16-bit row).
+  for (s.lg = 8; s.lg > 4; --s.lg) {
+    const uint32_t idle = cdiv(groups, 1u << s.lg) * (1u << s.lg) - groups;
+    if (idle * 8u <= groups) break;
+  }
+  while (s.lg > 0 && (1u << (s.lg - 1)) >= groups) --s.lg;
   const uint32_t teams = 256u >> s.lg, x = cdiv(groups, 1u << s.lg);
-  const uint32_t want = sums ? 1024u : 4096u;   // workgroups: few enough that their sums stay cheap
-  uint32_t y = cdiv(rows, teams * 4u), most = cdiv(want, x);
+  uint32_t y = cdiv(rows, teams * 4u), most = cdiv(sums ? 2048u : 4096u, x);
+  if (sums && most > 256u) most = 256u;   // the sums' own traffic stays small
   if (y > most) y = most;
   s.grid = dim3(x, y ? y : 1u);
   return s;
