@@ -35,17 +35,19 @@ __device__ __forceinline__ float sum8(f32x8 v) {
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
 
+// Sum over groups of N neighbouring lanes.
+template <int N = 64>
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  for (int d = N / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-// Sum over a team of L lanes (a workgroup's teams are whole waves; L > 64:
-// the team is the workgroup). `lds`: L / 64 floats of this call's own.
+// Sum over a team of L lanes: part of a wave, a wave, or (L > 64) the whole
+// workgroup. `lds`: L / 64 floats of this call's own.
 template <int L>
 __device__ __forceinline__ float team_sum(float v, float* lds) {
-  v = wave_sum(v);
+  v = wave_sum<L < 64 ? L : 64>(v);
   if constexpr (L > 64) {
     if ((threadIdx.x & 63u) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -101,9 +103,9 @@ __device__ __forceinline__ f32x8 centred(f32x8 v, float mean, int valid) {
 template <typename T, typename W, int L, int V, bool JOIN>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(RowsArgs a) {
   constexpr int R = L < 256 ? 256 / L : 1;
-  __shared__ float lds[2][L / 64];
+  __shared__ float lds[2][L < 64 ? 1 : L / 64];
   const uint32_t lane = threadIdx.x % L;
-  // Teams of one wave meet no barrier; a larger team is the workgroup, whose
+  // Teams of a wave or less meet no barrier; a larger team is the workgroup, whose
   // rows end together. Its two reductions alternate between two buffers.
   for (uint64_t r = (uint64_t)blockIdx.x * R + threadIdx.x / L; r < a.rows; r += (uint64_t)gridDim.x * R) {
     f32x8 v[V];
@@ -242,8 +244,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
       s1 += sum8(g);
       s2 += sum8(g * xh[i]);
     }
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
+    s1 = wave_sum<L < 64 ? L : 64>(s1);
+    s2 = wave_sum<L < 64 ? L : 64>(s2);
     if constexpr (L > 64) {
       if ((threadIdx.x & 63u) == 0) {
         lds[turn][0][threadIdx.x >> 6] = s1;
@@ -535,7 +537,9 @@ uint32_t row_groups(uint32_t teams) { return teams < kMaxGroups ? teams : kMaxGr
 
 // Workgroups of the backward norm kernel: one a CU.
 constexpr uint32_t kGradGroups = 256;
-constexpr uint32_t kGradCols = 16384;   // widest row whose sums stay in registers
+// Widest row whose sums stay in registers, one group a lane. Two groups spill:
+// 2048 x 16384 bf16 took 243 us, and takes 79 in two kernels.
+constexpr uint32_t kGradCols = 8192;
 
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream) {
   bool any = false;
@@ -563,9 +567,20 @@ hipError_t norm_typed(const RowsArgs& a, hipStream_t stream) {
     norm_kernel<T, W, L, V, JOIN><<<row_groups(cdiv(a.rows, R)), L < 256 ? 256 : L, 0, stream>>>(a);        \
     return hipGetLastError();                                                                               \
   }
+  ARX_NORM(8, 1)
+  ARX_NORM(32, 1)
   ARX_NORM(64, 1)
   ARX_NORM(64, 2)
   ARX_NORM(256, 1)
+  if constexpr (JOIN) {
+    // Few rows: one group a lane, so that a row's generator and sums take the
+    // least time (32 x 4096 bf16: 5.2 us against 6.5); many: fewer waves to
+    // meet (8192 x 8192: 143 us against 172).
+    if (a.rows <= 1024u) {
+      ARX_NORM(512, 1)
+      ARX_NORM(1024, 1)
+    }
+  }
   ARX_NORM(256, 2)
   ARX_NORM(256, 4)
   ARX_NORM(1024, 2)
@@ -608,12 +623,13 @@ hipError_t norm_grad_typed(const RowsGradArgs& a, hipStream_t stream) {
     if ((rc = hipGetLastError()) != hipSuccess) return rc;                                    \
     return launch_column_sum(s, stream);                                                      \
   }
+    ARX_NORM_GRAD(8, 1)
+    ARX_NORM_GRAD(32, 1)
     ARX_NORM_GRAD(64, 1)
     ARX_NORM_GRAD(128, 1)
     ARX_NORM_GRAD(256, 1)
     ARX_NORM_GRAD(512, 1)
     ARX_NORM_GRAD(1024, 1)
-    ARX_NORM_GRAD(1024, 2)
 #undef ARX_NORM_GRAD
   }
   NormGradWide<T, W, JOIN> op;
