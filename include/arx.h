@@ -377,6 +377,7 @@ int arx_rank(void);
  * arx_linear — y = act(z) + residual, z = x w^T + bias: x [m][k], w [n][k],
  * bias [n] or NULL, residual [m][n] or NULL, y [m][n], z [m][n] or NULL (kept
  * for arx_linear_backward). y may take residual's place.
+ *   m <= 2^29; n, k <= 2^22 - 8.
  *   workspace: 16-byte aligned device memory of at least
  *   arx_linear_workspace(m, n, k, aligned) bytes (0: may be NULL), used by
  *   this call alone until it has run. aligned: 1 if x and w start on 16-byte

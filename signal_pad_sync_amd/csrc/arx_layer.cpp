@@ -17,6 +17,9 @@ using arx::PlaneOut;
 using arx::set_error;
 
 constexpr size_t kMaxSize = 0x7FFFFFFF;
+// Of the linear calls: a tile's rows lie within 32-bit offsets of each other,
+// and a launch has fewer than 2^32 threads.
+constexpr size_t kMaxTokens = (size_t)1 << 29, kMaxWidth = ((size_t)1 << 22) - 8;
 
 size_t size_of(int dtype) { return dtype == ARX_F32 ? 4 : 2; }
 size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -130,18 +133,20 @@ int launched(hipError_t e, const char* what) {
 Plane plane(const void* p, size_t ld) { return {p, (int64_t)ld}; }
 PlaneOut plane_out(void* p, size_t ld) { return {p, (int64_t)ld}; }
 
-// The backward product's workspace: g, then what the two products and the
-// bias's column sums need one after another.
+// The backward pass's workspace: g, the operands that have to be copied, then
+// what the bias's column sums and the two products need one after another.
 struct LinearSpace {
-  size_t g = 0, rest = 0;
-  size_t total() const { return g + rest; }
+  size_t g = 0, pads = 0, rest = 0;
+  size_t total() const { return g + pads + rest; }
 };
 LinearSpace linear_space(size_t m, size_t n, size_t k, int act, bool aligned) {
+  const uint32_t m_ = (uint32_t)m, n_ = (uint32_t)n, k_ = (uint32_t)k;
   LinearSpace s;
   if (act != ARX_ACT_NONE) s.g = round_up(m * ((n + 7) & ~(size_t)7) * 2);
-  const size_t parts[3] = {arx::act_grad_workspace(m, n),
-                           arx::gemm_workspace((uint32_t)m, (uint32_t)k, (uint32_t)n, false, true, aligned),
-                           arx::gemm_workspace((uint32_t)n, (uint32_t)k, (uint32_t)m, true, true, aligned)};
+  else if (!aligned || n % 8) s.pads += arx::padded_bytes(m_, n_);
+  if (!aligned || k % 8) s.pads += arx::padded_bytes(m_, k_) + arx::padded_bytes(n_, k_);
+  const size_t parts[3] = {arx::act_grad_workspace(m, n), arx::gemm_splits_workspace(m_, k_, n_, false, true),
+                           arx::gemm_splits_workspace(n_, k_, m_, true, true)};
   for (size_t b : parts) s.rest = b > s.rest ? b : s.rest;
   return s;
 }
@@ -151,7 +156,9 @@ LinearSpace linear_space(size_t m, size_t n, size_t k, int act, bool aligned) {
 bool on_lines(const void* p, size_t ld) { return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && ld < ((size_t)1 << 22); }
 
 int check_linear(size_t m, size_t n, size_t k, int act, int dtype) {
-  TRY(check_sizes(m, n, k));
+  if (m > kMaxTokens) return set_error(ARX_EINVAL, "size m %zu above %zu", m, kMaxTokens);
+  if (n > kMaxWidth || k > kMaxWidth)
+    return set_error(ARX_EINVAL, "a size above %zu: n %zu, k %zu", kMaxWidth, n, k);
   if (dtype != ARX_BF16 && dtype != ARX_F16) return set_error(ARX_EINVAL, "dtype %d: ARX_BF16 or ARX_F16", dtype);
   if (act < ARX_ACT_NONE || act > ARX_ACT_SILU) return set_error(ARX_EINVAL, "act %d unknown", act);
   return ARX_OK;
@@ -162,8 +169,8 @@ int check_linear(size_t m, size_t n, size_t k, int act, int dtype) {
 extern "C" {
 
 size_t arx_linear_workspace(size_t m, size_t n, size_t k, int aligned) {
-  if (m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
-  return arx::gemm_workspace((uint32_t)m, (uint32_t)n, (uint32_t)k, false, false, aligned != 0);
+  if (m > kMaxTokens || n > kMaxWidth || k > kMaxWidth) return 0;
+  return arx::gemm_workspace((uint32_t)m, (uint32_t)n, (uint32_t)k, aligned != 0);
 }
 
 int arx_linear(const void* x, const void* w, const void* bias, const void* residual, void* y, void* z, size_t m,
@@ -196,7 +203,7 @@ int arx_linear(const void* x, const void* w, const void* bias, const void* resid
 }
 
 size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int aligned) {
-  if (m > kMaxSize || n > kMaxSize || k > kMaxSize) return 0;
+  if (m > kMaxTokens || n > kMaxWidth || k > kMaxWidth) return 0;
   return linear_space(m, n, k, act, aligned != 0).total();
 }
 
@@ -219,7 +226,8 @@ int arx_linear_backward(const void* dy, const void* x, const void* w, const void
              out("dw", dw, n, k, lddw, 2), out("dbias", dbias, 1, n, n, 2)}));
   const LinearSpace s = linear_space(m, n, k, act, on_lines(dy, lddy) && on_lines(x, ldx) && on_lines(w, ldw));
   TRY(check_workspace(workspace, workspace_bytes, s.total()));
-  char* const rest = static_cast<char*>(workspace) + s.g;
+  char* const pads = static_cast<char*>(workspace) + s.g;
+  char* const rest = pads + s.pads;
 
   const bool slope = act != ARX_ACT_NONE && (dx || dw);
   if (slope || dbias) {
@@ -233,33 +241,35 @@ int arx_linear_backward(const void* dy, const void* x, const void* w, const void
     a.partial = reinterpret_cast<float*>(rest);
     TRY(launched(arx::launch_act_grad(a, act, dtype, stream), "arx_linear_backward"));
   }
-  arx::GemmArgs g{};
-  g.a = slope ? workspace : dy;
-  g.lda = (int64_t)(slope ? (n + 7) & ~(size_t)7 : lddy);
-  g.a_whole = slope;
-  g.act = ARX_ACT_NONE;
-  g.workspace = rest;
-  if (dx) {
-    g.b = w;
-    g.ldb = (int64_t)ldw;
-    g.b_rows_k = true;
-    g.m = (uint32_t)m;
-    g.n = (uint32_t)k;
-    g.k = (uint32_t)n;
-    g.y = plane_out(dx, lddx);
-    TRY(launched(arx::launch_gemm(g, dtype, stream), "arx_linear_backward"));
-  }
-  if (dw) {
-    g.b = x;
-    g.ldb = (int64_t)ldx;
-    g.a_rows_k = g.b_rows_k = true;
-    g.m = (uint32_t)n;
-    g.n = (uint32_t)k;
-    g.k = (uint32_t)m;
-    g.y = plane_out(dw, lddw);
-    TRY(launched(arx::launch_gemm(g, dtype, stream), "arx_linear_backward"));
-  }
-  return ARX_OK;
+  if (!dx && !dw) return ARX_OK;
+
+  arx::Lines l[3] = {{slope ? workspace : dy, (int64_t)(slope ? (n + 7) & ~(size_t)7 : lddy), (uint32_t)m, (uint32_t)n, slope},
+                     {dx && some ? w : nullptr, (int64_t)ldw, (uint32_t)n, (uint32_t)k, false},
+                     {dw && some ? x : nullptr, (int64_t)ldx, (uint32_t)m, (uint32_t)k, false}};
+  if (some) TRY(launched(arx::launch_pad(l, 3, dtype, pads, stream), "arx_linear_backward"));
+  arx::GemmArgs gx{};
+  gx.a = l[0].p;
+  gx.lda = l[0].ld;
+  gx.a_whole = gx.b_whole = true;
+  gx.act = ARX_ACT_NONE;
+  gx.workspace = rest;
+  arx::GemmArgs gw = gx;
+  gx.b = l[1].p;
+  gx.ldb = l[1].ld;
+  gx.b_rows_k = true;
+  gx.m = (uint32_t)m;
+  gx.n = (uint32_t)k;
+  gx.k = (uint32_t)n;
+  gx.y = plane_out(dx, lddx);
+  gw.b = l[2].p;
+  gw.ldb = l[2].ld;
+  gw.a_rows_k = gw.b_rows_k = true;
+  gw.m = (uint32_t)n;
+  gw.n = (uint32_t)k;
+  gw.k = (uint32_t)m;
+  gw.y = plane_out(dw, lddw);
+  if (dx && dw) return launched(arx::launch_gemm_pair(gx, gw, dtype, stream), "arx_linear_backward");
+  return launched(arx::launch_gemm(dx ? gx : gw, dtype, stream), "arx_linear_backward");
 }
 
 int arx_layer_norm(const void* x, const void* weight, const void* shift, void* y, float* mean, float* rstd,

@@ -75,6 +75,22 @@ struct ActGradArgs {
 hipError_t launch_act_grad(const ActGradArgs& a, int act, int dtype, hipStream_t stream);
 size_t act_grad_workspace(size_t m, size_t n);
 
+// An operand as lines of contiguous elements. whole: its lines go on to a
+// multiple of eight elements, in zeros.
+struct Lines {
+  const void* p;
+  int64_t ld;
+  uint32_t lines, cols;
+  bool whole;
+};
+// Whether the tiles can load it as it stands: 16-byte chunks all the way, and
+// a tile's offsets within 32 bits.
+bool lines_as_is(const Lines& l);
+size_t padded_bytes(uint32_t lines, uint32_t cols);
+// Copies those of up to three that cannot be (nulls are let pass) to `space`,
+// padded_bytes() each, and points them there.
+hipError_t launch_pad(Lines* l, int count, int dtype, void* space, hipStream_t stream);
+
 // C[i][j] = sum over k of A(i, k) B(j, k), then the epilogue
 // z = C + bias[j] -> z; y = act(z) + residual -> y.
 // A(i, k) = a[i * lda + k], or a[k * lda + i] with a_rows_k; B the same.
@@ -82,7 +98,7 @@ struct GemmArgs {
   const void *a, *b;
   int64_t lda, ldb;
   bool a_rows_k, b_rows_k;
-  bool a_whole;  // a's lines go on to a multiple of eight elements, in zeros
+  bool a_whole, b_whole;  // as in Lines
   uint32_t m, n, k;
   const void* bias;
   Plane residual;
@@ -91,8 +107,13 @@ struct GemmArgs {
   void* workspace;
 };
 hipError_t launch_gemm(const GemmArgs& a, int dtype, hipStream_t stream);
-// aligned: both operands start on 16-byte boundaries and their ld is a
-// multiple of 8 below 2^22.
-size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned);
+// The products of a backward pass, operands as the tiles take them: one launch
+// or two. Their workspaces may be the same.
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, int dtype, hipStream_t stream);
+// Bytes for the forward product (aligned: both operands start on 16-byte
+// boundaries and their ld is a multiple of 8 below 2^22), and for the partial
+// sums of any product alone.
+size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool aligned);
+size_t gemm_splits_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k);
 
 }  // namespace arx

@@ -231,17 +231,19 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
 // so a lane's sums are neighbours in a row of C. The 16 x 16 x 32 instruction
 // moves a fifth less through the registers for a product than 32 x 32 x 16,
 // and where power bounds the clock that is time.
+template <int TM, int TN, int NS>
+constexpr int kTileBytes = NS * (TM + TN) * 128;
+
 template <typename T, int TM, int TN, int WM, int WN, int NS, bool A_ROWS_K, bool B_ROWS_K>
-__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+__device__ __forceinline__ void tile_body(const TileArgs& t, uint32_t id, char* lds) {
   constexpr int NW = WM * WN, MI = TM / WM / 16, NI = TN / WN / 16, BYTES = (TM + TN) * 128;
   constexpr int LA = TM / 8 / NW, LOADS = LA + TN / 8 / NW;
   constexpr int PITCH = TN / WN + 4;
   static_assert(NW * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
   static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
-  __shared__ __align__(1024) char lds[NS * BYTES];
   const GemmArgs& g = t.g;
   uint32_t ti, tj;
-  tile_of(blockIdx.x, t.tiles, t.tiles_n, &ti, &tj);
+  tile_of(id, t.tiles, t.tiles_n, &ti, &tj);
   const uint32_t i0 = ti * TM, j0 = tj * TN, lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = wave / WN * (TM / WM),
                  wj = wave % WN * (TN / WN);
@@ -375,6 +377,25 @@ __global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
   });
 }
 
+template <typename T, int TM, int TN, int WM, int WN, int NS, bool A_ROWS_K, bool B_ROWS_K>
+__global__ __launch_bounds__(WM * WN * 64) void tile_kernel(TileArgs t) {
+  __shared__ __align__(1024) char lds[kTileBytes<TM, TN, NS>];
+  tile_body<T, TM, TN, WM, WN, NS, A_ROWS_K, B_ROWS_K>(t, blockIdx.x, lds);
+}
+
+// The two products of a backward pass in one launch, dw's tiles (both operands
+// with their rows contiguous) and dx's: neither leaves CUs idle at its end, and
+// where one has few long tiles the other's short ones fill in beside them.
+template <typename T, bool DW_FIRST>
+__global__ __launch_bounds__(512) void pair_kernel(TileArgs dw, TileArgs dx) {
+  __shared__ __align__(1024) char lds[kTileBytes<256, 256, 2>];
+  const uint32_t first = DW_FIRST ? dw.tiles : dx.tiles;
+  if ((blockIdx.x < first) == DW_FIRST)
+    tile_body<T, 256, 256, 2, 4, 2, true, true>(dw, DW_FIRST ? blockIdx.x : blockIdx.x - first, lds);
+  else
+    tile_body<T, 256, 256, 2, 4, 2, false, true>(dx, DW_FIRST ? blockIdx.x - first : blockIdx.x, lds);
+}
+
 // ---- a few rows -------------------------------------------------------------
 
 // Up to 16 rows of A against 16 rows of B a workgroup, both with the depth
@@ -455,20 +476,20 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* part
 }
 
 // Lines copied to a distance that is a multiple of eight, zero past their end:
-// up to two operands in one launch.
+// up to three operands in one launch.
 struct PadArgs {
-  const void* p[2];
-  int64_t ld[2];
-  void* out[2];
-  uint32_t cols[2];
-  uint64_t items[2];   // groups of eight in all
+  const void* p[3];
+  int64_t ld[3];
+  void* out[3];
+  uint32_t cols[3];
+  uint64_t end[3];   // items (groups of eight) up to each one's last
 };
 template <typename T>
 __global__ __launch_bounds__(256) void pad_kernel(PadArgs a) {
   const uint64_t step = (uint64_t)gridDim.x * 256u;
-  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < a.items[0] + a.items[1]; e += step) {
-    const int w = e < a.items[0] ? 0 : 1;
-    const uint64_t item = w ? e - a.items[0] : e;
+  for (uint64_t e = (uint64_t)blockIdx.x * 256u + threadIdx.x; e < a.end[2]; e += step) {
+    const int w = e < a.end[0] ? 0 : (e < a.end[1] ? 1 : 2);
+    const uint64_t item = w ? e - a.end[w - 1] : e;
     const uint32_t cols = a.cols[w], across = cdiv(cols, 8), j = (uint32_t)(item % across) * 8u;
     const T* const from = static_cast<const T*>(a.p[w]) + (int64_t)(item / across) * a.ld[w] + j;
     store8<T>(static_cast<T*>(a.out[w]) + item * 8u, load8(from, cols - j < 8u ? (int)(cols - j) : 8), 8);
@@ -482,20 +503,13 @@ uint32_t grid_of(uint64_t items) {
   return (uint32_t)(groups < 8192 ? (groups ? groups : 1) : 8192);
 }
 
-// Whether the tiles can load an operand as it stands: 16-byte chunks all the
-// way, and a tile's offsets within 32 bits.
-bool loads_as_is(const void* p, int64_t ld, uint32_t contiguous) {
-  return ((uintptr_t)p & 15u) == 0 && ld % 8 == 0 && contiguous % 8 == 0 && ld < (1 << 22);
-}
-
-size_t padded_bytes(uint32_t rows, uint32_t cols) { return ((size_t)rows * (cdiv(cols, 8) * 8u) * 2u + 255) & ~(size_t)255; }
-
 // How a product is cut: the kernel, and workgroups along the depth.
 enum Cut { ROWS16, T64x64, T64x128, T128x128, T256x256, CUTS };
 struct Shape {
   int cut;
   uint32_t splits;
   uint32_t depth;   // of one split, a multiple of 64
+  float cost;       // microseconds
 };
 
 constexpr uint32_t kCus = 256;
@@ -520,8 +534,7 @@ constexpr float kJoin = 1.7f, kJoinSplit = 0.24f, kJoinBytes = 0.25e-6f;
 
 Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
   const uint32_t steps = cdiv(k ? k : 1, kDepth);
-  Shape best{T64x64, 1, steps * kDepth};
-  float least = 0.0f;
+  Shape best{T64x64, 1, steps * kDepth, 0.0f};
   // B streams past once for up to 16 rows of A: 9.7 us against 11.9 in tiles
   // at 1 x 4096 x 4096, 12.2 against 12.7 at 16 rows, 24 rows 13.9 against 12.8.
   const bool rows = m <= 16 && !a_rows_k && !b_rows_k;
@@ -538,10 +551,7 @@ Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k)
       const float waiting = t.wait * turns, busy = t.busy * per_cu;
       float cost = t.launch + (float)depth * (waiting > busy ? waiting : busy) + t.group * per_cu;
       if (splits > 1) cost += kJoin + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
-      if (least == 0.0f || cost < least) {
-        least = cost;
-        best = {c, splits, depth * kDepth};
-      }
+      if (best.cost == 0.0f || cost < best.cost) best = {c, splits, depth * kDepth, cost};
     }
   }
   return best;
@@ -565,6 +575,42 @@ hipError_t launch_rows(const TileArgs& t, uint32_t splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Copies the operands that the tiles cannot load as they stand to `space`,
+// which moves on, and points them there.
+template <typename T>
+hipError_t pad_lines(Lines* l, int count, char** space, hipStream_t stream) {
+  PadArgs pad{};
+  uint64_t items = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (i < count && l[i].p && !lines_as_is(l[i])) {
+      const uint32_t across = cdiv(l[i].cols, 8);
+      pad.p[i] = l[i].p;
+      pad.ld[i] = l[i].ld;
+      pad.out[i] = *space;
+      pad.cols[i] = l[i].cols;
+      items += (uint64_t)l[i].lines * across;
+      l[i].p = *space;
+      l[i].ld = (int64_t)across * 8;
+      l[i].whole = true;
+      *space += padded_bytes(l[i].lines, l[i].cols);
+    }
+    pad.end[i] = items;
+  }
+  if (items == 0) return hipSuccess;
+  pad_kernel<T><<<grid_of(items), 256, 0, stream>>>(pad);
+  return hipGetLastError();
+}
+
+// Whether one launch of 256 x 256 tiles takes less than two of their own.
+bool worth_pairing(uint32_t m, uint32_t n, uint32_t k) {
+  const CutCost& c = kCost[T256x256];
+  const uint64_t dx = (uint64_t)cdiv(m, 256) * cdiv(k, 256), dw = (uint64_t)cdiv(n, 256) * cdiv(k, 256);
+  const uint64_t dx_steps = cdiv(n, kDepth), dw_steps = cdiv(m, kDepth), longest = dx_steps > dw_steps ? dx_steps : dw_steps;
+  const uint64_t shared = (dx * dx_steps + dw * dw_steps + kCus - 1) / kCus;
+  const float cost = c.busy * (float)(shared > longest ? shared : longest) + c.group * (float)((dx + dw + kCus - 1) / kCus);
+  return cost < shape_of(m, k, n, false, true).cost + shape_of(n, k, m, true, true).cost;
+}
+
 template <typename T>
 hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   TileArgs t{};
@@ -574,25 +620,13 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   hipError_t rc = hipSuccess;
   char* space = static_cast<char*>(g.workspace);
   if (s.cut != ROWS16 && g.k > 0) {   // the tiles' loads go by whole chunks
-    PadArgs pad{};
-    const auto as_is = [&](int w, const void** p, int64_t* ld, bool rows_k, uint32_t rows, bool whole) {
-      const uint32_t lines = rows_k ? g.k : rows, contiguous = rows_k ? rows : g.k;
-      if (loads_as_is(*p, *ld, whole ? 0 : contiguous)) return;
-      pad.p[w] = *p;
-      pad.ld[w] = *ld;
-      pad.out[w] = space;
-      pad.cols[w] = contiguous;
-      pad.items[w] = (uint64_t)lines * cdiv(contiguous, 8);
-      *p = space;
-      *ld = (int64_t)cdiv(contiguous, 8) * 8;
-      space += padded_bytes(lines, contiguous);
-    };
-    as_is(0, &g.a, &g.lda, g.a_rows_k, g.m, g.a_whole);
-    as_is(1, &g.b, &g.ldb, g.b_rows_k, g.n, false);
-    if (pad.items[0] + pad.items[1] > 0) {
-      pad_kernel<T><<<grid_of(pad.items[0] + pad.items[1]), 256, 0, stream>>>(pad);
-      if ((rc = hipGetLastError()) != hipSuccess) return rc;
-    }
+    Lines l[2] = {{g.a, g.lda, g.a_rows_k ? g.k : g.m, g.a_rows_k ? g.m : g.k, g.a_whole},
+                  {g.b, g.ldb, g.b_rows_k ? g.k : g.n, g.b_rows_k ? g.n : g.k, g.b_whole}};
+    if ((rc = pad_lines<T>(l, 2, &space, stream)) != hipSuccess) return rc;
+    g.a = l[0].p;
+    g.lda = l[0].ld;
+    g.b = l[1].p;
+    g.ldb = l[1].ld;
   }
   t.depth = s.depth;
   t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;
@@ -608,19 +642,59 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   return hipGetLastError();
 }
 
+TileArgs whole_tiles(const GemmArgs& g) {
+  TileArgs t{};
+  t.g = g;
+  t.tiles_n = cdiv(g.n, 256);
+  t.tiles = cdiv(g.m, 256) * t.tiles_n;
+  t.depth = cdiv(g.k ? g.k : 1, kDepth) * kDepth;
+  return t;
+}
+
+template <typename T>
+hipError_t pair_typed(const GemmArgs& dx, const GemmArgs& dw, hipStream_t stream) {
+  const TileArgs tx = whole_tiles(dx), tw = whole_tiles(dw);
+  if (dw.k >= dx.k) pair_kernel<T, true><<<tx.tiles + tw.tiles, 512, 0, stream>>>(tw, tx);   // long tiles first
+  else pair_kernel<T, false><<<tx.tiles + tw.tiles, 512, 0, stream>>>(tw, tx);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+bool lines_as_is(const Lines& l) {
+  return ((uintptr_t)l.p & 15u) == 0 && l.ld % 8 == 0 && (l.whole || l.cols % 8 == 0) && l.ld < (1 << 22);
+}
+size_t padded_bytes(uint32_t lines, uint32_t cols) {
+  return ((size_t)lines * (cdiv(cols, 8) * 8u) * 2u + 255) & ~(size_t)255;
+}
+
+hipError_t launch_pad(Lines* l, int count, int dtype, void* space, hipStream_t stream) {
+  char* at = static_cast<char*>(space);
+  return dtype == ARX_BF16 ? pad_lines<__bf16>(l, count, &at, stream) : pad_lines<_Float16>(l, count, &at, stream);
+}
 
 hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t stream) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
   return dtype == ARX_BF16 ? gemm_typed<__bf16>(g, stream) : gemm_typed<_Float16>(g, stream);
 }
 
-size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool aligned) {
+hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, int dtype, hipStream_t stream) {
+  // dx: [m][k] over n; dw: [n][k] over m
+  if (dx.m > 0 && dx.n > 0 && dw.m > 0 && worth_pairing(dx.m, dw.m, dx.n))
+    return dtype == ARX_BF16 ? pair_typed<__bf16>(dx, dw, stream) : pair_typed<_Float16>(dx, dw, stream);
+  const hipError_t rc = launch_gemm(dx, dtype, stream);
+  return rc == hipSuccess ? launch_gemm(dw, dtype, stream) : rc;
+}
+
+size_t gemm_splits_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
   const Shape s = shape_of(m, n, k, a_rows_k, b_rows_k);
+  return s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0;
+}
+
+size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool aligned) {
+  const Shape s = shape_of(m, n, k, false, false);
   size_t bytes = s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0;
-  if (s.cut <= ROWS16) return bytes;
-  if (!aligned || (a_rows_k ? m : k) % 8) bytes += a_rows_k ? padded_bytes(k, m) : padded_bytes(m, k);
-  if (!aligned || (b_rows_k ? n : k) % 8) bytes += b_rows_k ? padded_bytes(k, n) : padded_bytes(n, k);
+  if (s.cut != ROWS16 && (!aligned || k % 8)) bytes += padded_bytes(m, k) + padded_bytes(n, k);
   return bytes;
 }
 
