@@ -92,7 +92,11 @@ struct Call {
   }
 
   PyObject* next() { return args[at++]; }
-  bool flag() { return next() == Py_True; }
+  bool flag() {
+    const int v = PyObject_IsTrue(next());
+    if (v < 0) throw python_error();
+    return v != 0;
+  }
   int number() {
     const long v = PyLong_AsLong(next());
     if (v == -1 && PyErr_Occurred()) throw python_error();

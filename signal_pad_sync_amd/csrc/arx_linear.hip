@@ -240,7 +240,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& t, uint32_t id, char* 
   constexpr int LA = TM / 8 / NW, LOADS = LA + TN / 8 / NW;
   constexpr int PITCH = TN / WN + 4;
   static_assert(NW * 32 * PITCH * 4 <= NS * BYTES, "the epilogue's blocks fit the buffers");
-  static_assert((NS - 2) * LOADS < 64, "the wait count fits its field");
+  static_assert((NS - 1) * LOADS < 64, "the wait count fits its field");
   const GemmArgs& g = t.g;
   uint32_t ti, tj;
   tile_of(id, t.tiles, t.tiles_n, &ti, &tj);

@@ -188,37 +188,30 @@ __device__ __forceinline__ float* partial_of(const RowsGradArgs& a, uint32_t wg,
 //   join: dresidual = dv, dx = dv dropped by the same bits, dbias = sum of dx.
 // A team takes every (gridDim.x R)-th row and keeps its columns' sums in
 // registers; the teams of a workgroup add theirs through shared memory.
-template <typename T, typename W, int L, int V, bool JOIN>
+template <typename T, typename W, int L, bool JOIN>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
   constexpr int R = 1024 / L;
   constexpr int SUMS = JOIN ? 3 : 2;
+  typedef typename Vec<T>::x8 x8;
   __shared__ float lds[2][2][16];
   __shared__ float gather[R > 1 ? 1024 * 8 : 1];
-  const uint32_t lane = threadIdx.x % L, team = threadIdx.x / L, groups = cdiv(a.cols, 8);
+  const uint32_t lane = threadIdx.x % L, team = threadIdx.x / L, groups = cdiv(a.cols, 8), c = lane * 8u;
+  const int there = valid_of(lane, a.cols);
   const float inv = 1.0f / (float)a.cols;
-  f32x8 w[V], sum[SUMS][V];
+  f32x8 w = f32x8(1.0f), sum[SUMS];
+  if (a.weight) w = widen(load8(static_cast<const W*>(a.weight) + c, there));
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const uint32_t g = lane + i * L;
-    w[i] = a.weight ? widen(load8(static_cast<const W*>(a.weight) + g * 8u, valid_of(g, a.cols))) : f32x8(1.0f);
-#pragma unroll
-    for (int k = 0; k < SUMS; ++k) sum[k][i] = f32x8(0.0f);
-  }
+  for (int k = 0; k < SUMS; ++k) sum[k] = f32x8(0.0f);
   // A row's values are asked for while the row before is worked on.
-  typedef typename Vec<T>::x8 x8;
-  x8 in_dy[V], in_x[V], in_dh[V];
+  x8 in_dy, in_x, in_dh;
   float in_mean = 0.0f, in_rstd = 0.0f;
   const auto ask = [&](uint64_t row) {
     const bool live = row < a.rows;
     const uint32_t r = live ? (uint32_t)row : 0u;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t g = lane + i * L;
-      const int valid = live ? valid_of(g, a.cols) : 0;
-      in_dy[i] = load8(row_of<T>(a.dy, r) + g * 8u, valid);
-      in_x[i] = load8(row_of<T>(a.x, r) + g * 8u, valid);
-      if (JOIN) in_dh[i] = load8(row_of<T>(a.dh, r) + g * 8u, a.dh.p ? valid : 0);
-    }
+    const int valid = live ? there : 0;
+    in_dy = load8(row_of<T>(a.dy, r) + c, valid);
+    in_x = load8(row_of<T>(a.x, r) + c, valid);
+    if (JOIN) in_dh = load8(row_of<T>(a.dh, r) + c, a.dh.p ? valid : 0);
     in_mean = live ? a.mean[r] : 0.0f;
     in_rstd = live ? a.rstd[r] : 0.0f;
   };
@@ -228,24 +221,14 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
   for (uint64_t base = (uint64_t)blockIdx.x * R; base < a.rows; base += stride, turn ^= 1) {
     const bool live = base + team < a.rows;
     const uint32_t r = live ? (uint32_t)base + team : 0u;
+    const int valid = live ? there : 0;
     const float mean = in_mean, rstd = in_rstd;
-    f32x8 dy[V], xh[V], dh[V];
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      dy[i] = widen(in_dy[i]);
-      xh[i] = centred(widen(in_x[i]), mean, live ? valid_of(lane + i * L, a.cols) : 0) * rstd;
-      if (JOIN) dh[i] = widen(in_dh[i]);
-    }
+    const f32x8 dy = widen(in_dy), xh = centred(widen(in_x), mean, valid) * rstd;
+    f32x8 dh;
+    if (JOIN) dh = widen(in_dh);
     if (base + stride < a.rows) ask(base + stride + team);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const f32x8 g = dy[i] * w[i];
-      s1 += sum8(g);
-      s2 += sum8(g * xh[i]);
-    }
-    s1 = wave_sum<L < 64 ? L : 64>(s1);
-    s2 = wave_sum<L < 64 ? L : 64>(s2);
+    const f32x8 g = dy * w;
+    float s1 = wave_sum<L < 64 ? L : 64>(sum8(g)), s2 = wave_sum<L < 64 ? L : 64>(sum8(g * xh));
     if constexpr (L > 64) {
       if ((threadIdx.x & 63u) == 0) {
         lds[turn][0][threadIdx.x >> 6] = s1;
@@ -261,39 +244,29 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
     }
     s1 *= inv;
     s2 *= inv;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t g = lane + i * L;
-      const int valid = live ? valid_of(g, a.cols) : 0;
-      f32x8 d = rstd * (dy[i] * w[i] - s1 - xh[i] * s2);
-      sum[0][i] += dy[i] * xh[i];
-      sum[1][i] += dy[i];
-      if constexpr (JOIN) {
-        if (a.dh.p) d += dh[i];
-        if (a.dresidual.p) store8<T>(row_of<T>(a.dresidual, r) + g * 8u, narrow<T>(d), valid);
-        if (valid > 0) d = drop8(d, (uint64_t)r * groups + g, a.drop);
-        if (valid > 0) sum[2][i] += d;
-      }
-      store8<T>(row_of<T>(a.dx, r) + g * 8u, narrow<T>(d), valid);
+    f32x8 d = rstd * (dy * w - s1 - xh * s2);
+    sum[0] += dy * xh;
+    sum[1] += dy;
+    if constexpr (JOIN) {
+      if (a.dh.p) d += dh;
+      if (a.dresidual.p) store8<T>(row_of<T>(a.dresidual, r) + c, narrow<T>(d), valid);
+      if (valid > 0) d = drop8(d, (uint64_t)r * groups + lane, a.drop);
+      if (valid > 0) sum[2] += d;
     }
+    store8<T>(row_of<T>(a.dx, r) + c, narrow<T>(d), valid);
   }
 #pragma unroll
   for (int k = 0; k < SUMS; ++k) {
     if ((k == 0 && !a.dweight) || (k == 1 && !a.dshift) || (k == 2 && !a.dbias)) continue;
-    float* const out = partial_of(a, blockIdx.x, SUMS, k);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t g = lane + i * L;
-      f32x8 s = sum[k][i];
-      if constexpr (R > 1) {
-        __syncthreads();
-        *reinterpret_cast<f32x8*>(&gather[threadIdx.x * 8u]) = s;
-        __syncthreads();
-        if (team == 0)
-          for (int t = 1; t < R; ++t) s += *reinterpret_cast<const f32x8*>(&gather[(t * L + lane) * 8u]);
-      }
-      if (team == 0) store8<float>(out + g * 8u, s, valid_of(g, a.cols));
+    f32x8 s = sum[k];
+    if constexpr (R > 1) {
+      __syncthreads();
+      *reinterpret_cast<f32x8*>(&gather[threadIdx.x * 8u]) = s;
+      __syncthreads();
+      if (team == 0)
+        for (int t = 1; t < R; ++t) s += *reinterpret_cast<const f32x8*>(&gather[(t * L + lane) * 8u]);
     }
+    if (team == 0) store8<float>(partial_of(a, blockIdx.x, SUMS, k) + c, s, there);
   }
 }
 
@@ -614,22 +587,22 @@ hipError_t norm_grad_typed(const RowsGradArgs& a, hipStream_t stream) {
   s.sums = JOIN ? 3 : 2;
   hipError_t rc;
   if (a.cols <= kGradCols) {
-#define ARX_NORM_GRAD(L, V)                                                                   \
-  if (groups <= L * V) {                                                                      \
+#define ARX_NORM_GRAD(L)                                                                      \
+  if (groups <= L) {                                                                          \
     constexpr uint32_t R = 1024 / L;                                                          \
     const uint32_t need = cdiv(a.rows, R);                                                    \
     s.groups = need < kGradGroups ? (need ? need : 1u) : kGradGroups;                         \
-    norm_grad_kernel<T, W, L, V, JOIN><<<s.groups, 1024, 0, stream>>>(a);                     \
+    norm_grad_kernel<T, W, L, JOIN><<<s.groups, 1024, 0, stream>>>(a);                        \
     if ((rc = hipGetLastError()) != hipSuccess) return rc;                                    \
     return launch_column_sum(s, stream);                                                      \
   }
-    ARX_NORM_GRAD(8, 1)
-    ARX_NORM_GRAD(32, 1)
-    ARX_NORM_GRAD(64, 1)
-    ARX_NORM_GRAD(128, 1)
-    ARX_NORM_GRAD(256, 1)
-    ARX_NORM_GRAD(512, 1)
-    ARX_NORM_GRAD(1024, 1)
+    ARX_NORM_GRAD(8)
+    ARX_NORM_GRAD(32)
+    ARX_NORM_GRAD(64)
+    ARX_NORM_GRAD(128)
+    ARX_NORM_GRAD(256)
+    ARX_NORM_GRAD(512)
+    ARX_NORM_GRAD(1024)
 #undef ARX_NORM_GRAD
   }
   NormGradWide<T, W, JOIN> op;
