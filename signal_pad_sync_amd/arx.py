@@ -412,7 +412,7 @@ def dropout_add(x, residual=None, bias=None, p=0.0, seed=0, offset=0, out=None, 
 
 def dropout_add_backward(dh, p=0.0, seed=0, offset=0, dbias=False, stream=None):
     """Gradients of dropout_add: (dx, dbias), dbias None unless asked for. The
-    residual's gradient is dh."""
+    residual's gradient is dh, and so is dx where p is 0."""
     return _run(_binding.dropout_add_backward, stream, dh, p, seed, offset, dbias)
 
 
@@ -426,5 +426,5 @@ def dropout_add_norm(x, residual=None, weight=None, shift=None, bias=None, p=0.0
 def dropout_add_norm_backward(dy, dh, h, mean, rstd, weight=None, p=0.0, seed=0, offset=0, dbias=False, stream=None):
     """Gradients of dropout_add_norm from y's (dy) and from h's other users
     (dh, or None): (dx, dresidual, dbias, dweight, dshift), dbias None unless
-    asked for."""
+    asked for. Where p is 0, dx and dresidual are one tensor."""
     return _run(_binding.dropout_add_norm_backward, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias)

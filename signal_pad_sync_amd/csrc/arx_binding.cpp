@@ -204,6 +204,9 @@ at::ScalarType norm_type(const Call& c, const at::Tensor* weight, const at::Tens
 
 bool on_lines(const Plane& a) { return ((uintptr_t)a.p & 15u) == 0 && a.ld % 8 == 0 && a.ld < ((size_t)1 << 22); }
 
+// Whether p rounds to no dropout at all (arx.h, arx_dropout_add).
+bool keeps_all(double p) { return p >= 0.0 && 65536.0 * p <= 0.5; }
+
 // ---- the operators -----------------------------------------------------------
 
 // (device, stream, x, w, bias, residual, act, save_z, out)
@@ -315,11 +318,12 @@ PyObject* dropout_add_backward(Call& c) {
   const bool want_db = c.flag();
   const int64_t rows = dh.size(0), cols = dh.size(1);
   const Plane dhp = c.plane(&dh, "dh", rows, cols);
-  const at::Tensor dx = c.empty({rows, cols}), db = want_db ? c.empty({cols}) : at::Tensor();
+  const bool same = keeps_all(p);   // dx is dh then
+  const at::Tensor dx = same ? dh : c.empty({rows, cols}), db = want_db ? c.empty({cols}) : at::Tensor();
   const size_t bytes = want_db ? g_arx.rows_workspace(rows, cols, 1) : 0;
   const at::Tensor space = c.space(bytes);
-  must(g_arx.dropout_add_backward(dhp.p, dx.data_ptr(), address(db), rows, cols, dhp.ld, cols, p, seed, offset, c.dtype,
-                                  address(space), bytes, c.stream));
+  must(g_arx.dropout_add_backward(dhp.p, same ? nullptr : dx.data_ptr(), address(db), rows, cols, dhp.ld, cols, p, seed,
+                                  offset, c.dtype, address(space), bytes, c.stream));
   return tuple({dx, db});
 }
 
@@ -366,12 +370,13 @@ PyObject* dropout_add_norm_backward(Call& c) {
               *const rp = (float*)c.vector(rstd, "rstd", rows, at::kFloat);
   void* const wp = c.vector(weight, "weight", cols, wt);
   const Plane dyp = c.plane(&dy, "dy", rows, cols);
-  const at::Tensor dx = c.empty({rows, cols}), dr = c.empty({rows, cols}),
+  const bool same = keeps_all(p);   // dresidual is dx then
+  const at::Tensor dx = c.empty({rows, cols}), dr = same ? dx : c.empty({rows, cols}),
                    db = want_db ? c.empty({cols}) : at::Tensor(), dw = c.empty({cols}, wt), ds = c.empty({cols}, wt);
   const size_t bytes = g_arx.rows_workspace(rows, cols, 3);
   const at::Tensor space = c.space(bytes);
-  must(g_arx.dropout_add_norm_backward(dyp.p, dhp.p, hp.p, mp, rp, wp, dx.data_ptr(), dr.data_ptr(), address(db),
-                                       dw.data_ptr(), ds.data_ptr(), rows, cols, dyp.ld, dhp.ld, hp.ld, cols, cols, p,
+  must(g_arx.dropout_add_norm_backward(dyp.p, dhp.p, hp.p, mp, rp, wp, dx.data_ptr(), same ? nullptr : dr.data_ptr(),
+                                       address(db), dw.data_ptr(), ds.data_ptr(), rows, cols, dyp.ld, dhp.ld, hp.ld, cols, cols, p,
                                        seed, offset, c.dtype, code_of(wt), address(space), bytes, c.stream));
   return tuple({dx, dr, db, dw, ds});
 }

@@ -285,6 +285,20 @@ def test_dropout_mask_is_the_generators(rows, cols, pad, p):
     assert torch.equal(h.cpu(), want)
 
 
+def test_no_dropout_copies_nothing():
+    """p = 0: the dropout's gradient is its argument, the join's two gradients
+    are one."""
+    dh = rand(1, 33, 72).cuda()
+    dx, db = arx.dropout_add_backward(dh, dbias=True)
+    assert dx is dh
+    R.close(db, *R.column_sum(dh.double().cpu(), torch.zeros(33, 72, dtype=torch.float64)))
+    h, y, mean, rstd = arx.dropout_add_norm(dh, dh)
+    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd)
+    assert dx is dr
+    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd, p=0.5)
+    assert dx is not dr
+
+
 def test_dropout_rate_and_independence():
     x = torch.ones(2048, 1024, dtype=BF16, device="cuda")
     n = x.numel()

@@ -128,8 +128,18 @@ def test_workspace_sizes():
         sizes = [L.arx_rows_workspace(rows, cols, k) for k in (1, 2, 3)]
         assert sizes[0] >= 4 * cols and sizes == sorted(sizes)
     # an activation's backward pass keeps one plane of gradients
-    plain, gelu = (L.arx_linear_backward_workspace(100, 64, 32, act, 0) for act in (0, 2))
+    plain, gelu = (L.arx_linear_backward_workspace(100, 64, 32, act, 1) for act in (0, 2))
     assert gelu >= plain + 100 * 64 * 2
+    # operands off 16-byte boundaries are copied onto them
+    assert L.arx_linear_workspace(100, 64, 32, 0) >= L.arx_linear_workspace(100, 64, 32, 1) + (100 + 64) * 32 * 2
+    assert L.arx_linear_workspace(100, 64, 33, 1) >= L.arx_linear_workspace(100, 64, 32, 1) + (100 + 64) * 40 * 2
+    assert L.arx_linear_backward_workspace(100, 64, 32, 0, 0) >= plain + (100 * 64 + 100 * 32 + 64 * 32) * 2
+
+
+@pytest.mark.parametrize("sizes", [dict(m=(1 << 29) + 1), dict(n=1 << 22), dict(k=(1 << 22) - 7)])
+def test_linear_size_limits(sizes):
+    assert linear(**sizes) == arx.EINVAL and linear_backward(**sizes) == arx.EINVAL
+    assert "size" in L.arx_strerror(arx.EINVAL).decode()
 
 
 def T(*shape, dtype=torch.bfloat16, strides=None):
