@@ -1,6 +1,7 @@
 /*
  * arx.h — C ABI of libarx: the one-shot W-way bf16 reduction gated by a
- * seq/parity flag protocol, and the blockwise signal-pad barrier, on one
+ * seq/parity flag protocol, the blockwise signal-pad barrier, and the
+ * operators of a tensor-parallel layer around the sum (at the end), on one
  * AMD Instinct MI355X (gfx950).
  *
  * The operation (page "arx.cu", protocol comment and arx_kernel): this GPU
