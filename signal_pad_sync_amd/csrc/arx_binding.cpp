@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <string>
+#include <utility>
 
 #include "arx.h"
 
@@ -165,6 +166,16 @@ struct Call {
 
   at::Tensor empty(at::IntArrayRef shape) const { return at::empty(shape, first.options()); }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType t) const { return at::empty(shape, first.options().dtype(t)); }
+  // Two vectors of n that are kept and dropped together (a row's statistics), in
+  // one allocation: one saves 0.7 us of the host's time.
+  std::pair<at::Tensor, at::Tensor> two(int64_t n, at::ScalarType t) const {
+    at::Tensor a = empty({2 * n}, t);
+    at::Tensor b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(a.storage()), a.key_set(), a.dtype());
+    a.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    b.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    b.unsafeGetTensorImpl()->set_storage_offset(n);
+    return {a, b};
+  }
   at::Tensor space(size_t bytes) const {
     return bytes ? at::empty({(int64_t)bytes}, first.options().dtype(at::kByte)) : at::Tensor();
   }
@@ -264,7 +275,7 @@ PyObject* layer_norm(Call& c) {
   void *const wp = c.vector(weight, "weight", cols, wt), *const sp = c.vector(shift, "shift", cols, wt);
   const Plane gp = c.plane(given, "out", rows, cols), xp = c.plane(&x, "x", rows, cols);
   const at::Tensor y = given ? *given : c.empty({rows, cols});
-  const at::Tensor mean = c.empty({rows}, at::kFloat), rstd = c.empty({rows}, at::kFloat);
+  const auto [mean, rstd] = c.two(rows, at::kFloat);
   must(g_arx.layer_norm(xp.p, wp, sp, y.data_ptr(), (float*)address(mean), (float*)address(rstd), rows, cols, xp.ld,
                         given ? gp.ld : cols, eps, c.dtype, code_of(wt), c.stream));
   return tuple({y, mean, rstd});
@@ -345,7 +356,7 @@ PyObject* dropout_add_norm(Call& c) {
              *const bp = c.vector(bias, "bias", cols, c.type);
   const Plane gp = c.plane(given, "out", rows, cols), xp = c.plane(&x, "x", rows, cols);
   const at::Tensor h = given ? *given : c.empty({rows, cols}), y = c.empty({rows, cols});
-  const at::Tensor mean = c.empty({rows}, at::kFloat), rstd = c.empty({rows}, at::kFloat);
+  const auto [mean, rstd] = c.two(rows, at::kFloat);
   must(g_arx.dropout_add_norm(xp.p, bp, rp.p, wp, sp, h.data_ptr(), y.data_ptr(), (float*)address(mean),
                               (float*)address(rstd), rows, cols, xp.ld, rp.ld, given ? gp.ld : cols, cols, eps, p, seed,
                               offset, c.dtype, code_of(wt), c.stream));
