@@ -300,6 +300,17 @@ __global__ __launch_bounds__(1024) void norm_stats_kernel(RowsGradArgs a) {
   }
 }
 
+// Where finished column sums go.
+struct SumsOut {
+  void* out[3];   // [cols] each, or null
+  int dtype[3];
+  __device__ __forceinline__ void put(int k, uint32_t c, float s) const {
+    if (dtype[k] == ARX_BF16) static_cast<__bf16*>(out[k])[c] = (__bf16)s;
+    else if (dtype[k] == ARX_F16) static_cast<_Float16*>(out[k])[c] = (_Float16)s;
+    else static_cast<float*>(out[k])[c] = s;
+  }
+};
+
 // ---- one thread per column group --------------------------------------------
 
 // 256 threads as 2^lg lanes over column groups by 256 >> lg rows; blockIdx.x
@@ -308,7 +319,8 @@ __global__ __launch_bounds__(1024) void norm_stats_kernel(RowsGradArgs a) {
 // in 40 us (5.0 TB/s). op.begin(group, valid) reads what a column keeps, op.row(r) works
 // on one row's group, and sums of kind k are op.sum[k].
 template <typename OP>
-__global__ __launch_bounds__(256) void column_kernel(OP op, uint32_t rows, uint32_t cols, int lg, float* partial) {
+__global__ __launch_bounds__(256) void column_kernel(OP op, uint32_t rows, uint32_t cols, int lg, float* partial,
+                                                     SumsOut sums) {
   __shared__ float gather[OP::SUMS > 0 ? 256 * 8 : 1];
   const uint32_t lanes = 1u << lg, lane = threadIdx.x & (lanes - 1u), team = threadIdx.x >> lg, teams = 256u >> lg;
   const uint32_t g = blockIdx.x * lanes + lane;
@@ -338,7 +350,14 @@ __global__ __launch_bounds__(256) void column_kernel(OP op, uint32_t rows, uint3
           for (uint32_t t = 1; t < teams; ++t)
             s += *reinterpret_cast<const f32x8*>(&gather[(t * lanes + lane) * 8u]);
       }
-      if (team == 0) store8<float>(partial + ((size_t)blockIdx.y * OP::SUMS + k) * cols + g * 8u, s, valid);
+      if (team != 0) continue;
+      if (gridDim.y > 1) {
+        store8<float>(partial + ((size_t)blockIdx.y * OP::SUMS + k) * cols + g * 8u, s, valid);
+      } else if (sums.out[k]) {   // all the rows: these are the sums
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < valid) sums.put(k, g * 8u + j, s[j]);
+      }
     }
   }
 }
@@ -457,8 +476,7 @@ struct ActGrad {
 
 struct ColumnSumArgs {
   const float* partial;  // [groups][sums][cols]
-  void* out[3];          // [cols] each, or null
-  int dtype[3];
+  SumsOut to;
   uint32_t groups, cols;
   int sums;
 };
@@ -468,7 +486,7 @@ struct ColumnSumArgs {
 __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSumArgs a) {
   __shared__ float lds[16][64];
   const int k = blockIdx.y;
-  if (!a.out[k]) return;
+  if (!a.to.out[k]) return;
   const uint32_t lane = threadIdx.x & 63u, slice = threadIdx.x >> 6, c = blockIdx.x * 64u + lane;
   float s = 0.0f;
   if (c < a.cols) {
@@ -481,15 +499,14 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSumArgs a) {
   s = 0.0f;
 #pragma unroll
   for (int q = 0; q < 16; ++q) s += lds[q][lane];
-  if (a.dtype[k] == ARX_BF16) static_cast<__bf16*>(a.out[k])[c] = (__bf16)s;
-  else if (a.dtype[k] == ARX_F16) static_cast<_Float16*>(a.out[k])[c] = (_Float16)s;
-  else static_cast<float*>(a.out[k])[c] = s;
+  a.to.put(k, c, s);
 }
 
 // ---- launches ---------------------------------------------------------------
 
 // Columns kernel geometry: lanes over a row's groups, and how many workgroups
 // share the rows.
+constexpr uint32_t kFewRows = 64;   // four a thread of the 16 teams
 struct ColumnShape {
   int lg;
   dim3 grid;
@@ -498,17 +515,20 @@ ColumnShape column_shape(uint32_t rows, uint32_t cols, bool sums) {
   const uint32_t groups = cdiv(cols, 8);
   ColumnShape s;
   // As many lanes across as leave at most an eighth of them idle, at least 16
-  // (256 consecutive bytes of a 16-bit row).
-  // With sums over many rows, at most 64: workgroups beside each other share
-  // the rows' split, so they fill the CUs at no cost in partial sums (dropout's
-  // backward pass of 16384 x 1024: 25.5 us with up to 256, 20.6).
-  for (s.lg = sums && rows > 1024u ? 6 : 8; s.lg > 4; --s.lg) {
+  // (256 consecutive bytes of a 16-bit row). With sums over many rows, at most
+  // 64: workgroups beside each other share the rows' split, so they fill the
+  // CUs at no cost in partial sums (dropout's backward pass of 16384 x 1024:
+  // 25.5 us with up to 256, 20.6). With sums over few, 16: one workgroup sees
+  // all the rows, and its sums are final (64 x 4096: 7.5 us in two kernels, 6.4
+  // in one; 128 x 1024: 7.4 and 7.7).
+  const bool few = sums && rows <= kFewRows;
+  for (s.lg = few ? 4 : sums && rows > 1024u ? 6 : 8; s.lg > 4; --s.lg) {
     const uint32_t idle = cdiv(groups, 1u << s.lg) * (1u << s.lg) - groups;
     if (idle * 8u <= groups) break;
   }
   while (s.lg > 0 && (1u << (s.lg - 1)) >= groups) --s.lg;
   const uint32_t teams = 256u >> s.lg, x = cdiv(groups, 1u << s.lg);
-  uint32_t y = cdiv(rows, teams * 4u), most = cdiv(sums ? 2048u : 4096u, x);
+  uint32_t y = few ? 1u : cdiv(rows, teams * 4u), most = cdiv(sums ? 2048u : 4096u, x);
   if (sums && most > 256u) most = 256u;   // the sums' own traffic stays small
   if (y > most) y = most;
   s.grid = dim3(x, y ? y : 1u);
@@ -527,19 +547,21 @@ constexpr uint32_t kGradCols = 8192;
 
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream) {
   bool any = false;
-  for (int k = 0; k < a.sums; ++k) any = any || a.out[k];
+  for (int k = 0; k < a.sums; ++k) any = any || a.to.out[k];
   if (!any || a.cols == 0) return hipSuccess;
   column_sum_kernel<<<dim3(cdiv(a.cols, 64), a.sums), 1024, 0, stream>>>(a);
   return hipGetLastError();
 }
 
+// The column kernel, and its sums' adding where several workgroups have parts.
 template <typename OP>
-hipError_t launch_column(const OP& op, uint32_t rows, uint32_t cols, float* partial, uint32_t* groups,
+hipError_t launch_column(const OP& op, uint32_t rows, uint32_t cols, float* partial, const SumsOut& to,
                          hipStream_t stream) {
   const ColumnShape s = column_shape(rows, cols, OP::SUMS > 0);
-  *groups = s.grid.y;
-  column_kernel<OP><<<s.grid, 256, 0, stream>>>(op, rows, cols, s.lg, partial);
-  return hipGetLastError();
+  column_kernel<OP><<<s.grid, 256, 0, stream>>>(op, rows, cols, s.lg, partial, to);
+  const hipError_t rc = hipGetLastError();
+  if (rc != hipSuccess || OP::SUMS == 0 || s.grid.y == 1) return rc;
+  return launch_column_sum({partial, to, s.grid.y, cols, OP::SUMS}, stream);
 }
 
 template <typename T, typename W, bool JOIN>
@@ -587,25 +609,18 @@ constexpr int code_of() {
 template <typename T, typename W, bool JOIN>
 hipError_t norm_grad_typed(const RowsGradArgs& a, hipStream_t stream) {
   const uint32_t groups = cdiv(a.cols, 8);
-  ColumnSumArgs s{};
-  s.partial = a.partial;
-  s.out[0] = a.dweight;
-  s.out[1] = a.dshift;
-  s.out[2] = JOIN ? a.dbias : nullptr;
-  s.dtype[0] = s.dtype[1] = code_of<W>();
-  s.dtype[2] = code_of<T>();
-  s.cols = a.cols;
-  s.sums = JOIN ? 3 : 2;
+  constexpr int SUMS = JOIN ? 3 : 2;
+  const SumsOut to = {{a.dweight, a.dshift, JOIN ? a.dbias : nullptr}, {code_of<W>(), code_of<W>(), code_of<T>()}};
   hipError_t rc;
   if (a.cols <= kGradCols) {
 #define ARX_NORM_GRAD(L)                                                                      \
   if (groups <= L) {                                                                          \
     constexpr uint32_t R = 1024 / L;                                                          \
     const uint32_t need = cdiv(a.rows, R);                                                    \
-    s.groups = need < kGradGroups ? (need ? need : 1u) : kGradGroups;                         \
-    norm_grad_kernel<T, W, L, JOIN><<<s.groups, 1024, 0, stream>>>(a);                        \
+    const uint32_t wgs = need < kGradGroups ? (need ? need : 1u) : kGradGroups;               \
+    norm_grad_kernel<T, W, L, JOIN><<<wgs, 1024, 0, stream>>>(a);                             \
     if ((rc = hipGetLastError()) != hipSuccess) return rc;                                    \
-    return launch_column_sum(s, stream);                                                      \
+    return launch_column_sum({a.partial, to, wgs, a.cols, SUMS}, stream);                     \
   }
     ARX_NORM_GRAD(8)
     ARX_NORM_GRAD(32)
@@ -618,13 +633,12 @@ hipError_t norm_grad_typed(const RowsGradArgs& a, hipStream_t stream) {
   }
   NormGradWide<T, W, JOIN> op;
   op.a = a;
-  op.a.stats = a.partial + wide_sums(a.rows, a.cols, s.sums);
+  op.a.stats = a.partial + wide_sums(a.rows, a.cols, SUMS);
   if (a.rows > 0) {
     norm_stats_kernel<T, W><<<row_groups(a.rows), 1024, 0, stream>>>(op.a);
     if ((rc = hipGetLastError()) != hipSuccess) return rc;
   }
-  if ((rc = launch_column(op, a.rows, a.cols, a.partial, &s.groups, stream)) != hipSuccess) return rc;
-  return launch_column_sum(s, stream);
+  return launch_column(op, a.rows, a.cols, a.partial, to, stream);
 }
 
 template <typename F>
@@ -656,32 +670,21 @@ hipError_t launch_dropout_add(const RowsArgs& a, int dtype, hipStream_t stream) 
   return by_types(dtype, dtype, [&](auto t, auto) {
     DropoutAdd<decltype(t)> op;
     op.a = a;
-    uint32_t groups;
-    return launch_column(op, a.rows, a.cols, nullptr, &groups, stream);
+    return launch_column(op, a.rows, a.cols, nullptr, SumsOut{}, stream);
   });
 }
 
 hipError_t launch_dropout_add_backward(const RowsGradArgs& a, int dtype, hipStream_t stream) {
   return by_types(dtype, dtype, [&](auto t, auto) {
     using T = decltype(t);
-    uint32_t groups;
     if (!a.dbias) {
       DropoutGrad<T, false> op;
       op.a = a;
-      return launch_column(op, a.rows, a.cols, nullptr, &groups, stream);
+      return launch_column(op, a.rows, a.cols, nullptr, SumsOut{}, stream);
     }
     DropoutGrad<T, true> op;
     op.a = a;
-    hipError_t rc = launch_column(op, a.rows, a.cols, a.partial, &groups, stream);
-    if (rc != hipSuccess) return rc;
-    ColumnSumArgs s{};
-    s.partial = a.partial;
-    s.out[0] = a.dbias;
-    s.dtype[0] = dtype;
-    s.groups = groups;
-    s.cols = a.cols;
-    s.sums = 1;
-    return launch_column_sum(s, stream);
+    return launch_column(op, a.rows, a.cols, a.partial, SumsOut{{a.dbias}, {dtype}}, stream);
   });
 }
 
@@ -694,24 +697,14 @@ size_t rows_workspace(size_t rows, size_t cols, int sums) {
 
 template <typename T, int ACT>
 static hipError_t act_grad_typed(const ActGradArgs& a, int dtype, hipStream_t stream) {
-  uint32_t groups;
   if (!a.dbias) {
     ActGrad<T, ACT, false> op;
     op.a = a;
-    return launch_column(op, a.m, a.n, nullptr, &groups, stream);
+    return launch_column(op, a.m, a.n, nullptr, SumsOut{}, stream);
   }
   ActGrad<T, ACT, true> op;
   op.a = a;
-  hipError_t rc = launch_column(op, a.m, a.n, a.partial, &groups, stream);
-  if (rc != hipSuccess) return rc;
-  ColumnSumArgs s{};
-  s.partial = a.partial;
-  s.out[0] = a.dbias;
-  s.dtype[0] = dtype;
-  s.groups = groups;
-  s.cols = a.n;
-  s.sums = 1;
-  return launch_column_sum(s, stream);
+  return launch_column(op, a.m, a.n, a.partial, SumsOut{{a.dbias}, {dtype}}, stream);
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, int act, int dtype, hipStream_t stream) {

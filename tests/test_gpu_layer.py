@@ -371,6 +371,36 @@ def test_dropout_add_norm(rows, cols, dtype, wdtype):
             R.close(db, *R.column_sum(v, e), "dbias")
 
 
+@pytest.mark.parametrize("rows", [63, 64, 65, 128, 129])
+@pytest.mark.parametrize("cols", [7, 136, 1001])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+def test_column_sums_by_one_workgroup_and_by_several(rows, cols, dtype):
+    """Bias gradients where their sums go from one kernel to two."""
+    note(f"column sums {rows}x{cols} {dtype}")
+    dh = rand(1, rows, cols, dtype=dtype)
+    mask = R.keep_mask(rows, cols, 0.2, SEED, OFFSET)
+    dx, db = arx.dropout_add_backward(dev(dh, 1), p=0.2, seed=SEED, offset=OFFSET, dbias=True)
+    want, e = R.dropout_add(dh, None, None, mask, R.scale_of(0.2))
+    R.close(dx, want, e, "dx")
+    R.close(db, *R.column_sum(want, e), "dbias")
+    x, w = rand(2, rows, 24, dtype=dtype), rand(3, cols, 24, dtype=dtype)
+    none = torch.zeros(rows, cols, dtype=torch.float64)
+    db = arx.linear_backward(dev(dh), dev(x), dev(w), dx=False, dw=False, dbias=True)[2]
+    R.close(db, *R.column_sum(dh.double(), none), "dbias of linear")
+
+
+@pytest.mark.parametrize("rows", [64, 65])
+def test_wide_norm_gradients_by_one_workgroup_and_by_several(rows):
+    cols = 8203
+    x, dy, w = rand(1, rows, cols), rand(2, rows, cols), rand(3, cols, dtype=F32, shift=1.0)
+    _, mean, rstd = arx.layer_norm(dev(x), dev(w))
+    dx, dw, ds = arx.layer_norm_backward(dev(dy), dev(x), mean, rstd, dev(w))
+    (d, de), vw, vs = R.norm_backward(dy, x, mean.cpu(), rstd.cpu(), w)
+    R.close(dx, d, de, "dx")
+    R.close(dw, *vw, "dweight")
+    R.close(ds, *vs, "dshift")
+
+
 def test_rows_of_nothing():
     x = torch.zeros(0, 24, dtype=BF16, device="cuda")
     assert arx.layer_norm(x)[0].shape == (0, 24)
