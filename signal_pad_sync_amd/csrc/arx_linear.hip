@@ -404,15 +404,16 @@ __global__ __launch_bounds__(512) void pair_kernel(TileArgs dw, TileArgs dx) {
 
 // Up to 16 rows of A against 16 rows of B a workgroup, both with the depth
 // contiguous and at any alignment. Bound by reading B once: it goes straight
-// to registers, and the sixteen waves take the depth's 64-deep chunks in turn,
-// so that a workgroup has all of a common depth under way at once; their sums
-// meet in shared memory. Four lanes read 64 consecutive bytes of a row. One
-// token of 4096 to 2048: 7.5 us, 16.8 MB in one burst and a latency; to 8192
-// from 8192: 28 us, 4.8 TB/s.
+// to registers, and the eight waves take the depth's 64-deep chunks in turn,
+// so that a workgroup has all of a depth of 2048 under way at once; their sums
+// meet in shared memory. Two workgroups share a CU, so one's loads run beside
+// the other's sums (sixteen waves: 8192 from 2048 12.2 us instead of 10.2,
+// 2048 from 4096 the same). Four lanes read 64 consecutive bytes of a row. One
+// token of 4096 to 2048: 8.8 us, 16.8 MB in two bursts; to 4096 from 2048: 6.9.
 template <typename T>
-__global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs t) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs t) {
   const GemmArgs& g = t.g;
-  constexpr int WAVES = 16, UNROLL = 4, PITCH = 20;
+  constexpr int WAVES = 8, PITCH = 20;
   typedef typename Vec<T>::x8 x8;
   __shared__ __align__(16) float lds[WAVES][16][PITCH];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 8u;
@@ -422,22 +423,28 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(4, 4))) vo
   const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r, g.n - 1u) * g.ldb + k_lane;
   f32x4 c = f32x4(0.0f);
   uint32_t s = k_first / 64u + wave;
-  for (; s + (UNROLL - 1) * WAVES < k_end / 64u; s += UNROLL * WAVES) {
-    x8 fb[UNROLL][2], fa[UNROLL][2];
+  // U chunks at once while the wave has as many whole ones
+  const auto bursts = [&](auto unroll) {
+    constexpr int U = decltype(unroll)::value;
+    for (; s + (U - 1) * WAVES < k_end / 64u; s += U * WAVES) {
+      x8 fb[U][2], fa[U][2];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fb[u][h] = load8(b + (s + u * WAVES) * 64u + h * 32, 8);
+        for (int h = 0; h < 2; ++h) fb[u][h] = load8(b + (s + u * WAVES) * 64u + h * 32, 8);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) fa[u][h] = load8(a + (s + u * WAVES) * 64u + h * 32, 8);
-    __builtin_amdgcn_sched_barrier(0);   // every load is under way before the first product waits
+        for (int h = 0; h < 2; ++h) fa[u][h] = load8(a + (s + u * WAVES) * 64u + h * 32, 8);
+      __builtin_amdgcn_sched_barrier(0);   // every load is under way before the first product waits
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c = mfma(fb[u][h], fa[u][h], c);
-  }
+        for (int h = 0; h < 2; ++h) c = mfma(fb[u][h], fa[u][h], c);
+    }
+  };
+  bursts(std::integral_constant<int, 4>{});
+  bursts(std::integral_constant<int, 2>{});
   for (; s * 64u < k_end; s += WAVES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -530,36 +537,45 @@ constexpr uint32_t kCus = 256;
 // fit to the times of 1100 cuts of 240 products (1 to 8192 rows, widths and
 // depths of 256 to 8192, the three layouts) on an MI355X; the cut with the
 // least cost by them is on average 1.5 % slower than the fastest one measured.
+// A step of the few-rows kernel grows with the rows of A that it reads again in
+// every workgroup, and beside it the tiles' cost is taken higher, as measured
+// where all of B comes from memory (60 products, 1 to 16 rows).
 struct CutCost {
   float launch, wait, busy, group;
   uint32_t tm, tn, resident;
 };
-constexpr CutCost kCost[CUTS] = {{1.4f, 0.112f, 0.115f, 2.0f, 16, 16, 1},
+constexpr CutCost kCost[CUTS] = {{2.3f, 0.100f, 0.105f, 0.42f, 16, 16, 2},
                                  {3.1f, 0.264f, 0.202f, 1.0f, 64, 64, 2},
                                  {3.2f, 0.437f, 0.329f, 1.6f, 64, 128, 2},
                                  {3.4f, 0.657f, 0.498f, 2.4f, 128, 128, 2},
                                  {0.0f, 1.224f, 1.242f, 11.2f, 256, 256, 1}};
-constexpr float kJoin = 1.7f, kJoinSplit = 0.24f, kJoinBytes = 0.25e-6f;
+constexpr float kRowOfA = 0.02f, kColdTiles = 1.15f;
+constexpr float kJoin = 1.7f, kJoinRows = 3.0f, kJoinSplit = 0.24f, kJoinBytes = 0.25e-6f;
 
-Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
+// as_is: the tiles can load both operands where they lie.
+Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool as_is) {
   const uint32_t steps = cdiv(k ? k : 1, kDepth);
   Shape best{T64x64, 1, steps * kDepth, 0.0f};
-  // B streams past once for up to 16 rows of A: 9.7 us against 11.9 in tiles
-  // at 1 x 4096 x 4096, 12.2 against 12.7 at 16 rows, 24 rows 13.9 against 12.8.
+  // Up to 16 rows of A, B can stream past once: one row, 4096 x 4096, 10.8 us
+  // against 13.3 in tiles; the tiles catch up where A or B is larger (16 rows,
+  // 12.5 and 13.3; 16 rows, 32000 x 2048, 36.0 and 28.3). Copying B for the
+  // tiles costs more than they save.
   const bool rows = m <= 16 && !a_rows_k && !b_rows_k;
-  for (int c = rows ? ROWS16 : T64x64; c < (rows ? T64x64 : CUTS); ++c) {
+  for (int c = rows ? ROWS16 : T64x64; c < (rows && !as_is ? T64x64 : CUTS); ++c) {
     const CutCost& t = kCost[c];
+    const float per_step = c == ROWS16 ? 1.0f + kRowOfA * (float)m : 1.0f;
     const uint64_t tiles = (uint64_t)cdiv(m, t.tm) * cdiv(n, t.tn);
     for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u}) {
-      // no split under 128 deep, nor where the CUs are taken as it is; half of
-      // them draw all that memory gives to B's rows
-      if (s > 1 && (steps < 2 * s || tiles * s > (c == ROWS16 ? kCus / 2 : 4 * kCus))) break;
+      // no split under 128 deep, nor where the CUs are taken as it is
+      if (s > 1 && (steps < 2 * s || tiles * s > (c == ROWS16 ? kCus : 4 * kCus))) break;
       const uint32_t depth = cdiv(steps, s), splits = cdiv(steps, depth);
       const float per_cu = (float)((tiles * splits + kCus - 1) / kCus);
       const float turns = (float)((uint32_t)(per_cu + t.resident - 1) / t.resident);
       const float waiting = t.wait * turns, busy = t.busy * per_cu;
-      float cost = t.launch + (float)depth * (waiting > busy ? waiting : busy) + t.group * per_cu;
-      if (splits > 1) cost += kJoin + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
+      float cost = t.launch + (float)depth * per_step * (waiting > busy ? waiting : busy) + t.group * per_cu;
+      if (splits > 1)
+        cost += (c == ROWS16 ? kJoinRows : kJoin) + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
+      if (rows && c != ROWS16) cost *= kColdTiles;
       if (best.cost == 0.0f || cost < best.cost) best = {c, splits, depth * kDepth, cost};
     }
   }
@@ -580,7 +596,7 @@ hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
 
 template <typename T>
 hipError_t launch_rows(const TileArgs& t, uint32_t splits, hipStream_t stream) {
-  rows_kernel<T><<<dim3(cdiv(t.g.n, 16), splits), 1024, 0, stream>>>(t);
+  rows_kernel<T><<<dim3(cdiv(t.g.n, 16), splits), 512, 0, stream>>>(t);
   return hipGetLastError();
 }
 
@@ -617,7 +633,7 @@ bool worth_pairing(uint32_t m, uint32_t n, uint32_t k) {
   const uint64_t dx_steps = cdiv(n, kDepth), dw_steps = cdiv(m, kDepth), longest = dx_steps > dw_steps ? dx_steps : dw_steps;
   const uint64_t shared = (dx * dx_steps + dw * dw_steps + kCus - 1) / kCus;
   const float cost = c.busy * (float)(shared > longest ? shared : longest) + c.group * (float)((dx + dw + kCus - 1) / kCus);
-  return cost < shape_of(m, k, n, false, true).cost + shape_of(n, k, m, true, true).cost;
+  return cost < shape_of(m, k, n, false, true, true).cost + shape_of(n, k, m, true, true, true).cost;
 }
 
 template <typename T>
@@ -625,12 +641,12 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   TileArgs t{};
   t.g = given;
   GemmArgs& g = t.g;
-  const Shape s = shape_of(g.m, g.n, g.k, g.a_rows_k, g.b_rows_k);
+  Lines l[2] = {{g.a, g.lda, g.a_rows_k ? g.k : g.m, g.a_rows_k ? g.m : g.k, g.a_whole},
+                {g.b, g.ldb, g.b_rows_k ? g.k : g.n, g.b_rows_k ? g.n : g.k, g.b_whole}};
+  const Shape s = shape_of(g.m, g.n, g.k, g.a_rows_k, g.b_rows_k, lines_as_is(l[0]) && lines_as_is(l[1]));
   hipError_t rc = hipSuccess;
   char* space = static_cast<char*>(g.workspace);
   if (s.cut != ROWS16 && g.k > 0) {   // the tiles' loads go by whole chunks
-    Lines l[2] = {{g.a, g.lda, g.a_rows_k ? g.k : g.m, g.a_rows_k ? g.m : g.k, g.a_whole},
-                  {g.b, g.ldb, g.b_rows_k ? g.k : g.n, g.b_rows_k ? g.n : g.k, g.b_whole}};
     if ((rc = pad_lines<T>(l, 2, &space, stream)) != hipSuccess) return rc;
     g.a = l[0].p;
     g.lda = l[0].ld;
@@ -695,16 +711,20 @@ hipError_t launch_gemm_pair(const GemmArgs& dx, const GemmArgs& dw, int dtype, h
   return rc == hipSuccess ? launch_gemm(dw, dtype, stream) : rc;
 }
 
+static size_t sums_of(const Shape& s, uint32_t m, uint32_t n) { return s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0; }
+
 size_t gemm_splits_workspace(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k) {
-  const Shape s = shape_of(m, n, k, a_rows_k, b_rows_k);
-  return s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0;
+  return sums_of(shape_of(m, n, k, a_rows_k, b_rows_k, true), m, n);
 }
 
 size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool aligned) {
-  const Shape s = shape_of(m, n, k, false, false);
-  size_t bytes = s.splits > 1 ? (size_t)s.splits * m * n * 4u : 0;
-  if (s.cut != ROWS16 && (!aligned || k % 8)) bytes += padded_bytes(m, k) + padded_bytes(n, k);
-  return bytes;
+  const Shape s = shape_of(m, n, k, false, false, true);
+  size_t bytes = sums_of(s, m, n);
+  if (aligned && k % 8 == 0) return bytes;
+  // enough as well where they are aligned after all
+  const Shape o = shape_of(m, n, k, false, false, false);
+  const size_t sums = sums_of(o, m, n) + (o.cut != ROWS16 ? padded_bytes(m, k) + padded_bytes(n, k) : 0);
+  return sums > bytes ? sums : bytes;
 }
 
 }  // namespace arx

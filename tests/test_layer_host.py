@@ -136,6 +136,13 @@ def test_workspace_sizes():
     assert L.arx_linear_backward_workspace(100, 64, 32, 0, 0) >= plain + (100 * 64 + 100 * 32 + 64 * 32) * 2
 
 
+@pytest.mark.parametrize("n", [8, 512, 4096, 5000, 32000])
+@pytest.mark.parametrize("k", [1, 64, 1000, 8192, 16384])
+def test_unaligned_workspace_serves_aligned_operands(n, k):
+    for m in (1, 2, 8, 16, 17, 64, 300):
+        assert L.arx_linear_workspace(m, n, k, 0) >= L.arx_linear_workspace(m, n, k, 1)
+
+
 @pytest.mark.parametrize("sizes", [dict(m=(1 << 29) + 1), dict(n=1 << 22), dict(k=(1 << 22) - 7)])
 def test_linear_size_limits(sizes):
     assert linear(**sizes) == arx.EINVAL and linear_backward(**sizes) == arx.EINVAL
