@@ -402,7 +402,7 @@ __global__ __launch_bounds__(512) void pair_kernel(TileArgs dw, TileArgs dx) {
 
 // ---- a few rows -------------------------------------------------------------
 
-// Up to 16 rows of A against 16 rows of B a workgroup, both with the depth
+// Up to 16 R rows of A against 16 rows of B a workgroup, both with the depth
 // contiguous and at any alignment. Bound by reading B once: it goes straight
 // to registers, and the eight waves take the depth's 64-deep chunks in turn,
 // so that a workgroup has all of a depth of 2048 under way at once; their sums
@@ -410,24 +410,29 @@ __global__ __launch_bounds__(512) void pair_kernel(TileArgs dw, TileArgs dx) {
 // the other's sums (sixteen waves: 8192 from 2048 12.2 us instead of 10.2,
 // 2048 from 4096 the same). Four lanes read 64 consecutive bytes of a row. One
 // token of 4096 to 2048: 8.8 us, 16.8 MB in two bursts; to 4096 from 2048: 6.9.
-template <typename T>
+// 32 tokens, 1024 to 1024: 5.9 us (7.9 in tiles, split and joined).
+template <typename T, int R>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs t) {
   const GemmArgs& g = t.g;
   constexpr int WAVES = 8, PITCH = 20;
   typedef typename Vec<T>::x8 x8;
-  __shared__ __align__(16) float lds[WAVES][16][PITCH];
+  __shared__ __align__(16) float lds[WAVES][16 * R][PITCH];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, r = lane & 15u, k_lane = (lane >> 4) * 8u;
   const uint32_t j0 = blockIdx.x * 16u;
   const uint32_t k_first = blockIdx.y * t.depth, k_end = min(g.k, k_first + t.depth);
-  const T* const a = static_cast<const T*>(g.a) + (int64_t)min(r, g.m - 1u) * g.lda + k_lane;
+  const T* a[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) a[q] = static_cast<const T*>(g.a) + (int64_t)min(r + 16u * q, g.m - 1u) * g.lda + k_lane;
   const T* const b = static_cast<const T*>(g.b) + (int64_t)min(j0 + r, g.n - 1u) * g.ldb + k_lane;
-  f32x4 c = f32x4(0.0f);
+  f32x4 c[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) c[q] = f32x4(0.0f);
   uint32_t s = k_first / 64u + wave;
   // U chunks at once while the wave has as many whole ones
   const auto bursts = [&](auto unroll) {
     constexpr int U = decltype(unroll)::value;
     for (; s + (U - 1) * WAVES < k_end / 64u; s += U * WAVES) {
-      x8 fb[U][2], fa[U][2];
+      x8 fb[U][2], fa[U][R][2];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -435,12 +440,16 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) fa[u][h] = load8(a + (s + u * WAVES) * 64u + h * 32, 8);
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) fa[u][q][h] = load8(a[q] + (s + u * WAVES) * 64u + h * 32, 8);
       __builtin_amdgcn_sched_barrier(0);   // every load is under way before the first product waits
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) c = mfma(fb[u][h], fa[u][h], c);
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) c[q] = mfma(fb[u][h], fa[u][q][h], c[q]);
     }
   };
   bursts(std::integral_constant<int, 4>{});
@@ -450,13 +459,16 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     for (int h = 0; h < 2; ++h) {
       const uint32_t k = s * 64u + h * 32u + k_lane;
       const int valid = k < k_end ? (int)min(8u, k_end - k) : 0;
-      c = mfma(load8(b + s * 64u + h * 32, valid), load8(a + s * 64u + h * 32, valid), c);
+      const x8 fb = load8(b + s * 64u + h * 32, valid);
+#pragma unroll
+      for (int q = 0; q < R; ++q) c[q] = mfma(fb, load8(a[q] + s * 64u + h * 32, valid), c[q]);
     }
   }
-  *reinterpret_cast<f32x4*>(&lds[wave][r][(lane >> 4) * 4u]) = c;
+#pragma unroll
+  for (int q = 0; q < R; ++q) *reinterpret_cast<f32x4*>(&lds[wave][r + 16 * q][(lane >> 4) * 4u]) = c[q];
   __syncthreads();
   const uint32_t i = threadIdx.x / 2u, j = threadIdx.x % 2u * 8u;
-  if (i >= 16u) return;
+  if (i >= 16u * R) return;
   f32x8 v = f32x8(0.0f);
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
@@ -520,7 +532,7 @@ uint32_t grid_of(uint64_t items) {
 }
 
 // How a product is cut: the kernel, and workgroups along the depth.
-enum Cut { ROWS16, T64x64, T64x128, T128x128, T256x256, CUTS };
+enum Cut { ROWS16, ROWS32, T64x64, T64x128, T128x128, T256x256, CUTS };
 struct Shape {
   int cut;
   uint32_t splits;
@@ -539,43 +551,47 @@ constexpr uint32_t kCus = 256;
 // least cost by them is on average 1.5 % slower than the fastest one measured.
 // A step of the few-rows kernel grows with the rows of A that it reads again in
 // every workgroup, and beside it the tiles' cost is taken higher, as measured
-// where all of B comes from memory (60 products, 1 to 16 rows).
+// where all of B comes from memory (90 products, 1 to 32 rows).
 struct CutCost {
   float launch, wait, busy, group;
   uint32_t tm, tn, resident;
 };
 constexpr CutCost kCost[CUTS] = {{2.3f, 0.100f, 0.105f, 0.42f, 16, 16, 2},
+                                 {2.3f, 0.100f, 0.105f, 0.42f, 32, 16, 2},
                                  {3.1f, 0.264f, 0.202f, 1.0f, 64, 64, 2},
                                  {3.2f, 0.437f, 0.329f, 1.6f, 64, 128, 2},
                                  {3.4f, 0.657f, 0.498f, 2.4f, 128, 128, 2},
                                  {0.0f, 1.224f, 1.242f, 11.2f, 256, 256, 1}};
-constexpr float kRowOfA = 0.02f, kColdTiles = 1.15f;
+constexpr float kRowOfA[T64x64] = {0.02f, 0.033f}, kColdTiles = 1.15f;
 constexpr float kJoin = 1.7f, kJoinRows = 3.0f, kJoinSplit = 0.24f, kJoinBytes = 0.25e-6f;
 
 // as_is: the tiles can load both operands where they lie.
 Shape shape_of(uint32_t m, uint32_t n, uint32_t k, bool a_rows_k, bool b_rows_k, bool as_is) {
   const uint32_t steps = cdiv(k ? k : 1, kDepth);
   Shape best{T64x64, 1, steps * kDepth, 0.0f};
-  // Up to 16 rows of A, B can stream past once: one row, 4096 x 4096, 10.8 us
-  // against 13.3 in tiles; the tiles catch up where A or B is larger (16 rows,
-  // 12.5 and 13.3; 16 rows, 32000 x 2048, 36.0 and 28.3). Copying B for the
-  // tiles costs more than they save.
-  const bool rows = m <= 16 && !a_rows_k && !b_rows_k;
-  for (int c = rows ? ROWS16 : T64x64; c < (rows && !as_is ? T64x64 : CUTS); ++c) {
+  // Up to 32 rows of A, B can stream past once: one row, 4096 x 4096, 10.8 us
+  // against 13.3 in tiles; 32 rows, 4096 x 1024, 6.6 and 8.7. The tiles catch up
+  // where A or B is larger (16 rows, 32000 x 2048, 36.0 and 28.3; 32 rows,
+  // 4096 x 4096, 16.8 and 13.6). Copying B for the tiles costs more than they
+  // save up to 16 rows (5001 x 2001, 23.4 and 24.8), not past them.
+  const bool across = !a_rows_k && !b_rows_k;
+  const int rows = across && m <= 16 ? ROWS16 : across && m <= 32 && as_is ? ROWS32 : CUTS;
+  for (int c = rows < CUTS ? rows : T64x64; c < (rows == ROWS16 && !as_is ? T64x64 : CUTS); ++c) {
+    if (c < T64x64 && c != rows) continue;
     const CutCost& t = kCost[c];
-    const float per_step = c == ROWS16 ? 1.0f + kRowOfA * (float)m : 1.0f;
+    const float per_step = c < T64x64 ? 1.0f + kRowOfA[c] * (float)m : 1.0f;
     const uint64_t tiles = (uint64_t)cdiv(m, t.tm) * cdiv(n, t.tn);
     for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u}) {
       // no split under 128 deep, nor where the CUs are taken as it is
-      if (s > 1 && (steps < 2 * s || tiles * s > (c == ROWS16 ? kCus : 4 * kCus))) break;
+      if (s > 1 && (steps < 2 * s || tiles * s > (c < T64x64 ? kCus : 4 * kCus))) break;
       const uint32_t depth = cdiv(steps, s), splits = cdiv(steps, depth);
       const float per_cu = (float)((tiles * splits + kCus - 1) / kCus);
       const float turns = (float)((uint32_t)(per_cu + t.resident - 1) / t.resident);
       const float waiting = t.wait * turns, busy = t.busy * per_cu;
       float cost = t.launch + (float)depth * per_step * (waiting > busy ? waiting : busy) + t.group * per_cu;
       if (splits > 1)
-        cost += (c == ROWS16 ? kJoinRows : kJoin) + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
-      if (rows && c != ROWS16) cost *= kColdTiles;
+        cost += (c < T64x64 ? kJoinRows : kJoin) + kJoinSplit * splits + kJoinBytes * 4.0f * (splits + 1) * (float)m * (float)n;
+      if (rows < CUTS && c >= T64x64) cost *= kColdTiles;
       if (best.cost == 0.0f || cost < best.cost) best = {c, splits, depth * kDepth, cost};
     }
   }
@@ -594,9 +610,9 @@ hipError_t launch_tiles(TileArgs t, uint32_t splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, int R>
 hipError_t launch_rows(const TileArgs& t, uint32_t splits, hipStream_t stream) {
-  rows_kernel<T><<<dim3(cdiv(t.g.n, 16), splits), 512, 0, stream>>>(t);
+  rows_kernel<T, R><<<dim3(cdiv(t.g.n, 16), splits), 512, 0, stream>>>(t);
   return hipGetLastError();
 }
 
@@ -646,7 +662,7 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   const Shape s = shape_of(g.m, g.n, g.k, g.a_rows_k, g.b_rows_k, lines_as_is(l[0]) && lines_as_is(l[1]));
   hipError_t rc = hipSuccess;
   char* space = static_cast<char*>(g.workspace);
-  if (s.cut != ROWS16 && g.k > 0) {   // the tiles' loads go by whole chunks
+  if (s.cut >= T64x64 && g.k > 0) {   // the tiles' loads go by whole chunks
     if ((rc = pad_lines<T>(l, 2, &space, stream)) != hipSuccess) return rc;
     g.a = l[0].p;
     g.lda = l[0].ld;
@@ -656,7 +672,8 @@ hipError_t gemm_typed(const GemmArgs& given, hipStream_t stream) {
   t.depth = s.depth;
   t.partial = s.splits > 1 ? reinterpret_cast<float*>(space) : nullptr;
   switch (s.cut) {
-    case ROWS16: rc = launch_rows<T>(t, s.splits, stream); break;
+    case ROWS16: rc = launch_rows<T, 1>(t, s.splits, stream); break;
+    case ROWS32: rc = launch_rows<T, 2>(t, s.splits, stream); break;
     case T64x64: rc = launch_tiles<T, 64, 64, 2, 2, 4>(t, s.splits, stream); break;
     case T64x128: rc = launch_tiles<T, 64, 128, 2, 2, 3>(t, s.splits, stream); break;
     case T128x128: rc = launch_tiles<T, 128, 128, 2, 2, 2>(t, s.splits, stream); break;
@@ -723,7 +740,7 @@ size_t gemm_workspace(uint32_t m, uint32_t n, uint32_t k, bool aligned) {
   if (aligned && k % 8 == 0) return bytes;
   // enough as well where they are aligned after all
   const Shape o = shape_of(m, n, k, false, false, false);
-  const size_t sums = sums_of(o, m, n) + (o.cut != ROWS16 ? padded_bytes(m, k) + padded_bytes(n, k) : 0);
+  const size_t sums = sums_of(o, m, n) + (o.cut >= T64x64 ? padded_bytes(m, k) + padded_bytes(n, k) : 0);
   return sums > bytes ? sums : bytes;
 }
 

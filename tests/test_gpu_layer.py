@@ -58,12 +58,14 @@ SIZES = [(1, 1, 1), (1, 64, 8), (1, 2048, 512), (2, 100, 1000), (3, 17, 33), (5,
          (255, 256, 64), (256, 512, 1024), (257, 300, 200), (300, 1, 65), (1, 300, 4096), (511, 513, 130), (1024, 8, 8)]
 
 
-# up to 16 tokens: past weights streamed once, with the depth whole and split,
+# up to 32 tokens: past weights streamed once, with the depth whole and split,
 # and in tiles, which take weights on 16-byte boundaries only
 @pytest.mark.parametrize("pad", [0, 3, 8])
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 2048), (1, 512, 8192), (2, 500, 16384), (5, 300, 4096), (8, 5000, 2000),
                                    (16, 9000, 520), (16, 20000, 72), (3, 16384, 1024), (16, 2048, 8192),
-                                   (16, 1024, 2056), (16, 1025, 4100), (7, 33000, 130)])
+                                   (16, 1024, 2056), (16, 1025, 4100), (7, 33000, 130),
+                                   (17, 1024, 1024), (24, 4097, 1032), (31, 250, 520), (32, 700, 4096), (32, 40, 72),
+                                   (32, 4096, 2048), (33, 1024, 1024)])
 def test_few_tokens(m, n, k, pad):
     check_linear(m, n, k, F16 if n % 3 else BF16, "silu", bias=True, residual=True, save_z=True, pad=pad)
 
