@@ -512,7 +512,7 @@ struct ColumnShape {
   dim3 grid;
 };
 ColumnShape column_shape(uint32_t rows, uint32_t cols, bool sums) {
-  const uint32_t groups = cdiv(cols, 8);
+  const uint32_t groups = cols ? cdiv(cols, 8) : 1u;   // nothing is launched over no columns
   ColumnShape s;
   // As many lanes across as leave at most an eighth of them idle, at least 16
   // (256 consecutive bytes of a 16-bit row). With sums over many rows, at most
@@ -557,6 +557,7 @@ hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream) {
 template <typename OP>
 hipError_t launch_column(const OP& op, uint32_t rows, uint32_t cols, float* partial, const SumsOut& to,
                          hipStream_t stream) {
+  if (cols == 0) return hipSuccess;
   const ColumnShape s = column_shape(rows, cols, OP::SUMS > 0);
   column_kernel<OP><<<s.grid, 256, 0, stream>>>(op, rows, cols, s.lg, partial, to);
   const hipError_t rc = hipGetLastError();
