@@ -408,7 +408,7 @@ size_t arx_linear_backward_workspace(size_t m, size_t n, size_t k, int act, int 
  * arx_layer_norm — over each row of x [rows][cols]: y = (x - mean) rstd
  * weight + shift, rstd = 1 / sqrt(variance + eps), the variance divided by
  * cols. weight, shift [cols] or NULL (1 and 0); mean, rstd: f32 [rows] out,
- * or NULL. y may take x's place. eps >= 0.
+ * or NULL (NaN where cols is 0). y may take x's place. eps >= 0.
  */
 int arx_layer_norm(const void* x, const void* weight, const void* shift, void* y, float* mean, float* rstd,
                    size_t rows, size_t cols, size_t ldx, size_t ldy, double eps, int dtype, int wdtype,

@@ -278,9 +278,9 @@ int arx_layer_norm(const void* x, const void* weight, const void* shift, void* y
   TRY(check_sizes(rows, cols));
   TRY(check_types(dtype, wdtype));
   TRY(check_eps(eps));
-  if (rows == 0 || cols == 0) return ARX_OK;
-  TRY(need("x", x));
-  TRY(need("y", y));
+  if (rows == 0 || (cols == 0 && !mean && !rstd)) return ARX_OK;
+  TRY(need("x", x, cols > 0));
+  TRY(need("y", y, cols > 0));
   const size_t e = size_of(dtype), we = size_of(wdtype);
   TRY(check({in("x", x, rows, cols, ldx, e, true), in("weight", weight, 1, cols, cols, we),
              in("shift", shift, 1, cols, cols, we), out("y", y, rows, cols, ldy, e), out("mean", mean, 1, rows, rows, 4),
@@ -389,9 +389,9 @@ int arx_dropout_add_norm(const void* x, const void* bias, const void* residual, 
   TRY(check_eps(eps));
   arx::RowsArgs a{};
   TRY(make_drop(p, seed, offset, &a.drop));
-  if (rows == 0 || cols == 0) return ARX_OK;
-  TRY(need("x", x));
-  TRY(need("y", y));
+  if (rows == 0 || (cols == 0 && !mean && !rstd)) return ARX_OK;
+  TRY(need("x", x, cols > 0));
+  TRY(need("y", y, cols > 0));
   const size_t e = size_of(dtype), we = size_of(wdtype);
   TRY(check({in("x", x, rows, cols, ldx, e, true), in("bias", bias, 1, cols, cols, e),
              in("residual", residual, rows, cols, ldr, e, true), in("weight", weight, 1, cols, cols, we),

@@ -42,3 +42,25 @@ def test_linear_gradients_with_a_dimension_of_zero(m, n, k, act):
                                    dx=want[0], dw=want[1])
         for t, full, asked in zip(part, got, want):
             assert torch.equal(t, full) if asked else t is None
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (F16, F32), (F32, F32)], ids=["bf16", "f16-f32", "f32"])
+@pytest.mark.parametrize("rows", [1, 5, 1000])
+def test_statistics_of_no_columns(rows, dtype, wdtype):
+    """The mean of nothing is NaN, and so is what follows from it; neither is
+    what the memory held before."""
+    note(f"norms {rows}x0 {dtype}")
+    x, w = torch.zeros(rows, 0, dtype=dtype, device="cuda"), torch.zeros(0, dtype=wdtype, device="cuda")
+    for call in (lambda: arx.layer_norm(x, w, w), lambda: arx.dropout_add_norm(x, x, w, w, bias=x[0], p=0.5)[1:],
+                 lambda: arx.dropout_add_norm(x)[1:]):
+        before = torch.full((2 * rows,), 7.0, device="cuda")
+        del before                       # the statistics take its place
+        y, mean, rstd = call()
+        assert y.shape == (rows, 0) and torch.isnan(mean).all() and torch.isnan(rstd).all()
+    stats = torch.full((2, rows), 7.0, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert arx.lib.arx_layer_norm(None, None, None, None, stats[0].data_ptr(), None, rows, 0, 0, 0, 1e-5, arx.BF16,
+                                  arx.BF16, stream) == 0
+    assert arx.lib.arx_dropout_add_norm(None, None, None, None, None, None, None, None, stats[1].data_ptr(), rows, 0,
+                                        0, 0, 0, 0, 1e-5, 0.1, 1, 2, arx.F32, arx.F32, stream) == 0
+    assert torch.isnan(stats).all()
