@@ -410,10 +410,11 @@ def dropout_add(x, residual=None, bias=None, p=0.0, seed=0, offset=0, out=None, 
     return _run(_binding.dropout_add, stream, x, residual, bias, p, seed, offset, out)
 
 
-def dropout_add_backward(dh, p=0.0, seed=0, offset=0, dbias=False, stream=None):
+def dropout_add_backward(dh, p=0.0, seed=0, offset=0, dbias=False, stream=None, share=False):
     """Gradients of dropout_add: (dx, dbias), dbias None unless asked for. The
-    residual's gradient is dh, and so is dx where p is 0."""
-    return _run(_binding.dropout_add_backward, stream, dh, p, seed, offset, dbias)
+    residual's gradient is dh. share: where p is 0, dx may be dh itself (for
+    callers that change neither in place); else it has memory of its own."""
+    return _run(_binding.dropout_add_backward, stream, dh, p, seed, offset, dbias, share)
 
 
 def dropout_add_norm(x, residual=None, weight=None, shift=None, bias=None, p=0.0, seed=0, offset=0, eps=1e-5,
@@ -423,8 +424,11 @@ def dropout_add_norm(x, residual=None, weight=None, shift=None, bias=None, p=0.0
     return _run(_binding.dropout_add_norm, stream, x, residual, weight, shift, bias, p, seed, offset, eps, out)
 
 
-def dropout_add_norm_backward(dy, dh, h, mean, rstd, weight=None, p=0.0, seed=0, offset=0, dbias=False, stream=None):
+def dropout_add_norm_backward(dy, dh, h, mean, rstd, weight=None, p=0.0, seed=0, offset=0, dbias=False, stream=None,
+                              share=False):
     """Gradients of dropout_add_norm from y's (dy) and from h's other users
     (dh, or None): (dx, dresidual, dbias, dweight, dshift), dbias None unless
-    asked for. Where p is 0, dx and dresidual are one tensor."""
-    return _run(_binding.dropout_add_norm_backward, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias)
+    asked for. share: where p is 0, dx and dresidual may be one tensor (for
+    callers that change neither in place); else each has memory of its own."""
+    return _run(_binding.dropout_add_norm_backward, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias,
+                share)

@@ -321,15 +321,15 @@ PyObject* dropout_add(Call& c) {
   return THPVariable_Wrap(h);
 }
 
-// (device, stream, dh, p, seed, offset, dbias)
+// (device, stream, dh, p, seed, offset, dbias, share)
 PyObject* dropout_add_backward(Call& c) {
   const at::Tensor& dh = c.lead("dh", false);
   const double p = c.real();
   const uint64_t seed = c.bits("seed"), offset = c.bits("offset");
-  const bool want_db = c.flag();
+  const bool want_db = c.flag(), share = c.flag();
   const int64_t rows = dh.size(0), cols = dh.size(1);
   const Plane dhp = c.plane(&dh, "dh", rows, cols);
-  const bool same = keeps_all(p);   // dx is dh then
+  const bool same = share && keeps_all(p);   // dx is dh then
   const at::Tensor dx = same ? dh : c.empty({rows, cols}), db = want_db ? c.empty({cols}) : at::Tensor();
   const size_t bytes = want_db ? g_arx.rows_workspace(rows, cols, 1) : 0;
   const at::Tensor space = c.space(bytes);
@@ -363,7 +363,7 @@ PyObject* dropout_add_norm(Call& c) {
   return tuple({h, y, mean, rstd});
 }
 
-// (device, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias)
+// (device, stream, dy, dh, h, mean, rstd, weight, p, seed, offset, dbias, share)
 PyObject* dropout_add_norm_backward(Call& c) {
   const at::Tensor& dy = c.lead("dy", false);
   const at::Tensor* const dh = c.tensor("dh", true);
@@ -373,7 +373,7 @@ PyObject* dropout_add_norm_backward(Call& c) {
   const at::Tensor* const weight = c.tensor("weight", true);
   const double p = c.real();
   const uint64_t seed = c.bits("seed"), offset = c.bits("offset");
-  const bool want_db = c.flag();
+  const bool want_db = c.flag(), share = c.flag();
   const int64_t rows = dy.size(0), cols = dy.size(1);
   const at::ScalarType wt = norm_type(c, weight, nullptr);
   const Plane dhp = c.plane(dh, "dh", rows, cols), hp = c.plane(h, "h", rows, cols);
@@ -381,7 +381,7 @@ PyObject* dropout_add_norm_backward(Call& c) {
               *const rp = (float*)c.vector(rstd, "rstd", rows, at::kFloat);
   void* const wp = c.vector(weight, "weight", cols, wt);
   const Plane dyp = c.plane(&dy, "dy", rows, cols);
-  const bool same = keeps_all(p);   // dresidual is dx then
+  const bool same = share && keeps_all(p);   // dresidual is dx then
   const at::Tensor dx = c.empty({rows, cols}), dr = same ? dx : c.empty({rows, cols}),
                    db = want_db ? c.empty({cols}) : at::Tensor(), dw = c.empty({cols}, wt), ds = c.empty({cols}, wt);
   const size_t bytes = g_arx.rows_workspace(rows, cols, 3);
@@ -452,9 +452,9 @@ PyMethodDef methods[] = {
     method<layer_norm, 7>("layer_norm"),
     method<layer_norm_backward, 7>("layer_norm_backward"),
     method<dropout_add, 9>("dropout_add"),
-    method<dropout_add_backward, 7>("dropout_add_backward"),
+    method<dropout_add_backward, 8>("dropout_add_backward"),
     method<dropout_add_norm, 12>("dropout_add_norm"),
-    method<dropout_add_norm_backward, 12>("dropout_add_norm_backward"),
+    method<dropout_add_norm_backward, 13>("dropout_add_norm_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -298,16 +298,16 @@ def test_dropout_mask_is_the_generators(rows, cols, pad, p):
 
 
 def test_no_dropout_copies_nothing():
-    """p = 0: the dropout's gradient is its argument, the join's two gradients
-    are one."""
+    """p = 0 and a caller that lets them be shared: the dropout's gradient is its
+    argument, the join's two gradients are one."""
     dh = rand(1, 33, 72).cuda()
-    dx, db = arx.dropout_add_backward(dh, dbias=True)
+    dx, db = arx.dropout_add_backward(dh, dbias=True, share=True)
     assert dx is dh
     R.close(db, *R.column_sum(dh.double().cpu(), torch.zeros(33, 72, dtype=torch.float64)))
     h, y, mean, rstd = arx.dropout_add_norm(dh, dh)
-    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd)
+    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd, share=True)
     assert dx is dr
-    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd, p=0.5)
+    dx, dr, _, _, _ = arx.dropout_add_norm_backward(dh, None, h, mean, rstd, p=0.5, share=True)
     assert dx is not dr
 
 

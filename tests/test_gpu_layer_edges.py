@@ -1,11 +1,11 @@
 """GPU: the layer operators where a dimension is zero, against their
-definitions (tests/layer_ref.py)."""
+definitions (tests/layer_ref.py), and whose memory their results are."""
 import pytest
 import torch
 
 from signal_pad_sync_amd import arx
 from tests import layer_ref as R
-from tests.gpu_util import note
+from tests.gpu_util import library, note
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,46 @@ def test_statistics_of_no_columns(rows, dtype, wdtype):
     assert arx.lib.arx_dropout_add_norm(None, None, None, None, None, None, None, None, stats[1].data_ptr(), rows, 0,
                                         0, 0, 0, 0, 1e-5, 0.1, 1, 2, arx.F32, arx.F32, stream) == 0
     assert torch.isnan(stats).all()
+
+
+@pytest.mark.parametrize("p", [0.0, 2.0 ** -18, 0.25])
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("other", [False, True], ids=["current", "stream"])
+def test_gradients_own_their_memory(p, pad, other):
+    """Whatever p is: each gradient contiguous and memory of its own, so that
+    changing one in place changes neither another nor an argument."""
+    note(f"gradients' memory p={p} pad={pad} other stream={other}")
+    buf = torch.randn(33, 72 + pad, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    dh = buf[:, :72]
+    h, y, mean, rstd = arx.dropout_add_norm(dh, dh)
+    torch.cuda.synchronize()
+    kept = buf.clone()
+    s = torch.cuda.Stream() if other else None
+    for dbias in (False, True):
+        dx, _ = arx.dropout_add_backward(dh, p=p, dbias=dbias, stream=s)
+        dxn, dr, _, _, _ = arx.dropout_add_norm_backward(dh, dh, h, mean, rstd, p=p, dbias=dbias, stream=s)
+        torch.cuda.synchronize()
+        outs = [dx, dxn, dr]
+        want = [t.clone() for t in outs]
+        if p < 2.0 ** -17:
+            assert torch.equal(dx, dh) and torch.equal(dxn, dr)
+        for i, t in enumerate(outs):
+            assert t.is_contiguous()
+            t.zero_()
+            for j in range(i + 1, len(outs)):
+                assert torch.equal(outs[j], want[j])
+            assert torch.equal(buf, kept)
+        torch.cuda.synchronize()
+
+
+def test_gradients_of_no_dropout_take_the_all_reduce():
+    """A column slice's gradient is a plane that arx.allreduce takes."""
+    dh = torch.randn(8, 80, generator=torch.Generator().manual_seed(2)).to(BF16).cuda()[:, :64]
+    with library(2, 512):
+        for src in (1,):
+            arx.recv_view(1, src, 512).zero_()
+        dx, _ = arx.dropout_add_backward(dh)
+        out = torch.empty_like(dx)
+        arx.allreduce(dx, out, 512)
+        torch.cuda.synchronize()
+        assert torch.equal(out, dh)
