@@ -20,11 +20,10 @@
 #include "arx_elem.h"
 #include "arx_internal.h"
 #include "arx_layer.h"
+#include "arx_shapes.h"
 
 namespace arx {
 namespace {
-
-__host__ __device__ constexpr uint32_t cdiv(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 
 __device__ __forceinline__ int valid_of(uint32_t group, uint32_t cols) {
   const uint32_t c = group * 8u;
@@ -504,37 +503,6 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(ColumnSumArgs a) {
 
 // ---- launches ---------------------------------------------------------------
 
-// Columns kernel geometry: lanes over a row's groups, and how many workgroups
-// share the rows.
-constexpr uint32_t kFewRows = 64;   // four a thread of the 16 teams
-struct ColumnShape {
-  int lg;
-  dim3 grid;
-};
-ColumnShape column_shape(uint32_t rows, uint32_t cols, bool sums) {
-  const uint32_t groups = cols ? cdiv(cols, 8) : 1u;   // nothing is launched over no columns
-  ColumnShape s;
-  // As many lanes across as leave at most an eighth of them idle, at least 16
-  // (256 consecutive bytes of a 16-bit row). With sums over many rows, at most
-  // 64: workgroups beside each other share the rows' split, so they fill the
-  // CUs at no cost in partial sums (dropout's backward pass of 16384 x 1024:
-  // 25.5 us with up to 256, 20.6). With sums over few, 16: one workgroup sees
-  // all the rows, and its sums are final (64 x 4096: 7.5 us in two kernels, 6.4
-  // in one; 128 x 1024: 7.4 and 7.7).
-  const bool few = sums && rows <= kFewRows;
-  for (s.lg = few ? 4 : sums && rows > 1024u ? 6 : 8; s.lg > 4; --s.lg) {
-    const uint32_t idle = cdiv(groups, 1u << s.lg) * (1u << s.lg) - groups;
-    if (idle * 8u <= groups) break;
-  }
-  while (s.lg > 0 && (1u << (s.lg - 1)) >= groups) --s.lg;
-  const uint32_t teams = 256u >> s.lg, x = cdiv(groups, 1u << s.lg);
-  uint32_t y = few ? 1u : cdiv(rows, teams * 4u), most = cdiv(sums ? 2048u : 4096u, x);
-  if (sums && most > 256u) most = 256u;   // the sums' own traffic stays small
-  if (y > most) y = most;
-  s.grid = dim3(x, y ? y : 1u);
-  return s;
-}
-
 // A launch has fewer than 2^32 threads; past that many rows, teams loop.
 constexpr uint32_t kMaxGroups = 1u << 20;
 uint32_t row_groups(uint32_t teams) { return teams < kMaxGroups ? teams : kMaxGroups; }
@@ -559,10 +527,10 @@ hipError_t launch_column(const OP& op, uint32_t rows, uint32_t cols, float* part
                          hipStream_t stream) {
   if (cols == 0) return hipSuccess;
   const ColumnShape s = column_shape(rows, cols, OP::SUMS > 0);
-  column_kernel<OP><<<s.grid, 256, 0, stream>>>(op, rows, cols, s.lg, partial, to);
+  column_kernel<OP><<<dim3(s.x, s.y), 256, 0, stream>>>(op, rows, cols, s.lg, partial, to);
   const hipError_t rc = hipGetLastError();
-  if (rc != hipSuccess || OP::SUMS == 0 || s.grid.y == 1) return rc;
-  return launch_column_sum({partial, to, s.grid.y, cols, OP::SUMS}, stream);
+  if (rc != hipSuccess || OP::SUMS == 0 || s.y == 1) return rc;
+  return launch_column_sum({partial, to, s.y, cols, OP::SUMS}, stream);
 }
 
 template <typename T, typename W, bool JOIN>
@@ -599,7 +567,7 @@ hipError_t norm_typed(const RowsArgs& a, hipStream_t stream) {
 
 // Floats of a wide backward pass's column sums, in front of its row sums.
 size_t wide_sums(uint32_t rows, uint32_t cols, int sums) {
-  return ((size_t)column_shape(rows, cols, true).grid.y * sums * cols + 3) & ~(size_t)3;
+  return ((size_t)column_shape(rows, cols, true).y * sums * cols + 3) & ~(size_t)3;
 }
 
 template <typename T>
@@ -722,7 +690,7 @@ hipError_t launch_act_grad(const ActGradArgs& a, int act, int dtype, hipStream_t
 }
 
 size_t act_grad_workspace(size_t m, size_t n) {
-  return ((column_shape((uint32_t)m, (uint32_t)n, true).grid.y * n + 3) & ~(size_t)3) * 4;
+  return ((column_shape((uint32_t)m, (uint32_t)n, true).y * n + 3) & ~(size_t)3) * 4;
 }
 
 }  // namespace arx
