@@ -112,7 +112,8 @@ inline ColumnShape column_shape(uint32_t rows, uint32_t cols, bool sums) {
   // 25.5 us with up to 256, 20.6). With sums over few, 16: one workgroup sees
   // all the rows, and its sums are final (64 x 4096: 7.5 us in two kernels, 6.4
   // in one; 128 x 1024: 7.4 and 7.7).
-  const bool few = sums && rows <= kFewRows;
+  // Not past 2^23 such workgroups: a launch has fewer than 2^32 threads.
+  const bool few = sums && rows <= kFewRows && groups <= 1u << 27;
   for (s.lg = few ? 4 : sums && rows > 1024u ? 6 : 8; s.lg > 4; --s.lg) {
     const uint32_t idle = cdiv(groups, 1u << s.lg) * (1u << s.lg) - groups;
     if (idle * 8u <= groups) break;

@@ -107,3 +107,14 @@ def test_gradients_of_no_dropout_take_the_all_reduce():
         arx.allreduce(dx, out, 512)
         torch.cuda.synchronize()
         assert torch.equal(out, dh)
+
+
+def test_column_sums_of_the_widest_plane():
+    """2^31 - 1 columns, the largest size: one row's bias gradient is the row."""
+    cols = (1 << 31) - 1
+    note(f"dropout_add_backward 1x{cols}")
+    dh = torch.empty(1, cols, dtype=BF16, device="cuda")
+    dh.view(-1)[: 1 << 30].normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    dh.view(-1)[1 << 30:] = dh.view(-1)[: cols - (1 << 30)].neg()
+    dx, db = arx.dropout_add_backward(dh, dbias=True)
+    assert torch.equal(db, dh[0]) and torch.equal(dx, dh)

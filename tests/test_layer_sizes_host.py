@@ -73,3 +73,18 @@ def test_splits_cover_the_depth(shapes, m, n, k):
     for layout in ("fwd", "dx", "dw"):
         for as_is in (False, True):
             cut_of(shapes, (m, n, k), layout, as_is)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 17, 64, 65, 1025, 1 << 20, (1 << 31) - 1])
+@pytest.mark.parametrize("cols", [1, 8, 127, 4096, 1 << 22, (1 << 28) + 8, (1 << 31) - 129, (1 << 31) - 1])
+@pytest.mark.parametrize("sums", [False, True])
+def test_column_walks_fit_a_launch(shapes, rows, cols, sums):
+    """Every column has a lane, and a launch has fewer than 2^32 threads in x:
+    256 a workgroup here, and 1024 for 64 columns where several workgroups'
+    sums are added."""
+    out = (ctypes.c_uint64 * 3)()
+    shapes.columns_of(ctypes.c_uint32(rows), ctypes.c_uint32(cols), sums, out)
+    lanes, x, y = out
+    assert x * lanes * 8 >= cols and 1 <= y < 1 << 16
+    assert x * 256 < 1 << 32
+    assert not sums or y == 1 or -(-cols // 64) * 1024 < 1 << 32
