@@ -89,12 +89,18 @@ __device__ const uint4 kZeros = {0, 0, 0, 0};
 // wait for every LDS read under way at the next use of any; the instruction
 // itself has no result register, and the waits for it are written out
 // (wait_and_meet). It stays between the statements that it stands between.
+// m0 holds a load's LDS address and is written right before it; the compiler
+// keeps nothing of its own there across a statement, and the clobber tells it
+// not to. It warns at every use that m0 is a register that it reserves.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds(const char* base, uint32_t off, uint32_t block) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(block), "v"(off), "s"(base) : "m0");
 }
 __device__ __forceinline__ void to_lds(const void* p, uint32_t block) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(block), "v"(p) : "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
