@@ -13,24 +13,20 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__bf16> {
   typedef bf16x8 x8;
-  typedef __bf16 x4 __attribute__((ext_vector_type(4)));
 };
 template <>
 struct Vec<_Float16> {
   typedef f16x8 x8;
-  typedef _Float16 x4 __attribute__((ext_vector_type(4)));
 };
 template <>
 struct Vec<float> {
   typedef f32x8 x8;
-  typedef f32x4 x4;
 };
 
 // Eight consecutive elements from p on, the first `valid` of them read and the
