@@ -353,7 +353,8 @@ int arx_rank(void);
  *     wdtype, the type of a norm's weight and shift: dtype or ARX_F32.
  *   - a plane of rows is a pointer and a row distance ld >= cols in elements:
  *     element (r, c) at p[r * ld + c]. Any element-aligned address and any
- *     ld will do; a vector (bias, weight, shift, mean, ...) is contiguous.
+ *     ld up to 2^31 - 1 will do; a vector (bias, weight, shift, mean, ...) is
+ *     contiguous.
  *   - sizes are 0 .. 2^31 - 1 each. Nothing is launched where every output is
  *     empty; a sum over no rows is written as zero.
  *   - sums, means and variances are binary32; each output is rounded once,
@@ -361,7 +362,8 @@ int arx_rank(void);
  *   - an output may take an input plane's place (same address, same ld) where
  *     the call says so; any other overlap of an output with anything else is
  *     ARX_EINVAL.
- *   - sums run in a fixed order: the same call gives the same bits.
+ *   - sums run in a fixed order: the same call gives the same bits (an
+ *     operand's alignment is part of the call: another may take another order).
  * Errors of all of them (nothing launched): ARX_EINVAL, ARX_EHIP.
  */
 #define ARX_BF16 0
@@ -394,8 +396,10 @@ size_t arx_linear_workspace(size_t m, size_t n, size_t k, int aligned);
  * arx_linear_backward — with g = dy act'(z): dx [m][k] = g w, dw [n][k] =
  * g^T x, dbias [n] = sum over rows of g (dresidual is dy). Any of dx, dw and
  * dbias may be NULL; x is read for dw, w for dx, z unless act is
- * ARX_ACT_NONE, and those that are not read may be NULL. g enters the
- * products rounded to dtype, and dbias as it is.
+ * ARX_ACT_NONE, and those that are not read may be NULL. With an activation g
+ * enters the products rounded to dtype (over terms without a common sign that
+ * puts dx and dw 1.4 times their own rounding off, in the root mean square),
+ * and dbias as it is.
  *   workspace: as for arx_linear, arx_linear_backward_workspace(...) bytes;
  *   aligned: of dy, x and w.
  */

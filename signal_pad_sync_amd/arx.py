@@ -358,7 +358,13 @@ def pad_view(rank: int):
 # Planes are 2-D tensors whose rows are contiguous (stride(1) == 1, any row
 # stride); vectors are contiguous; all are on the current device. Outputs that
 # the caller does not pass, and workspaces, come from torch's allocator. Calls
-# run on the current stream, or on `stream`, whose memory the outputs then are.
+# run on the current stream, or on `stream`, whose memory the outputs then are; a
+# tensor of another stream's has to be ready by then, and kept (or recorded with
+# Tensor.record_stream) until the call has run.
+#
+# Autograd does not see these calls: forward and backward are calls of their own,
+# and a result of tensors that require a gradient has no graph behind it. A module
+# wraps the two in a torch.autograd.Function.
 
 
 def _act(act):

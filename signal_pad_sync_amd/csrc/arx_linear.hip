@@ -233,9 +233,12 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles, uint32_t ti
 // next NS - 1 are under way. B's fragments take the matrix instruction's rows,
 // so a lane's sums are neighbours in a row of C. The 16 x 16 x 32 instruction
 // moves a fifth less through the registers for a product than 32 x 32 x 16,
-// and where power bounds the clock that is time: 8192^3 in 750 us (1467
-// TFLOP/s) plain, 833 with gelu, bias, residual and z, three quarters of the
-// matrix cores' cycles at the clock that the power leaves. Eight waves of
+// and where power bounds the clock that is time: 8192^3 in 750 to 810 us
+// by card (1467 to 1353 TFLOP/s) plain, 831 to 893 with gelu, bias, residual and
+// z; the matrix cores are busy in 72 to 77 % and 70 to 72 % of the cycles, at the
+// clock that the power leaves. A few hundred rows fill the chip once or less,
+// and then a step waits for its loads: 1024 x 4096 x 4096 in 128 x 128 tiles, two
+// buffers, takes 61 us with the matrix cores busy in 25 % of the cycles. Eight waves of
 // 128 x 64 read 192 KiB of LDS a step, as long as its products take; four of
 // 128 x 128 would read 128 and have no registers left.
 template <int TM, int TN, int NS>
@@ -412,7 +415,9 @@ __global__ __launch_bounds__(512) void pair_kernel(TileArgs dw, TileArgs dx) {
 // meet in shared memory. Two workgroups share a CU, so one's loads run beside
 // the other's sums (sixteen waves: 8192 from 2048 12.2 us instead of 10.2,
 // 2048 from 4096 the same). Four lanes read 64 consecutive bytes of a row. One
-// token of 4096 to 2048: 8.8 us, 16.8 MB in two bursts; to 4096 from 2048: 6.9.
+// token of 4096 to 2048: 8.6 us, of which a workgroup's two bursts, the launch
+// and the sums' meeting take 6.4 (4096 to 256, memory idle); to 4096 from 2048, one
+// burst, 7.0. Every workgroup reads all of x: 32 tokens of 2048 to 4096 take 10.2.
 // 32 tokens, 1024 to 1024: 5.9 us (7.9 in tiles, split and joined).
 template <typename T, int R>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void rows_kernel(TileArgs t) {
@@ -505,9 +510,9 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, const float* part
 }
 
 // Lines copied to a distance that is a multiple of eight, zero past their end:
-// up to three operands in one launch (333 x 1001 and 777 x 1001: 2.4 us). The
-// tiles' loads take whole 16-byte chunks; a staged load of odd rows would cost
-// every tile more than the copy does.
+// up to three operands in one launch, since the tiles' loads take whole 16-byte
+// chunks. 333 x 1001 and 777 x 1001: 3.7 us, and a product of 12.8 that takes 8.6
+// from 1000 on 16-byte boundaries.
 struct PadArgs {
   const void* p[3];
   int64_t ld[3];

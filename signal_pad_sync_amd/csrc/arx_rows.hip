@@ -99,9 +99,9 @@ __device__ __forceinline__ f32x8 centred(f32x8 v, float mean, int valid) {
 
 // A row in registers, V groups of eight a lane: one read, the mean, then the
 // mean of the squared distances from it (no cancellation), one write. Bound by
-// memory: 8192 x 8192 bf16 in 53 us (5.1 TB/s), the join of 8192 x 4096 in 62
-// (4.3 TB/s, the generator's integer products beside it); a few rows take one
-// memory latency and two reductions, 32 x 4096 in 4.8 us.
+// memory: 8192 x 8192 bf16 in 53 us (5.1 TB/s), the join of 8192 x 4096 in 58
+// to 62 (4.6 to 4.3 TB/s, the generator's integer products beside it); a few rows
+// take one memory latency and two reductions, 32 x 4096 in 3.8 us back to back.
 template <typename T, typename W, int L, int V, bool JOIN>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_kernel(RowsArgs a) {
   constexpr int R = L < 256 ? 256 / L : 1;
@@ -190,9 +190,14 @@ __device__ __forceinline__ float* partial_of(const RowsGradArgs& a, uint32_t wg,
 //   join: dresidual = dv, dx = dv dropped by the same bits, dbias = sum of dx.
 // A team takes every (gridDim.x R)-th row and keeps its columns' sums in
 // registers; the teams of a workgroup add theirs through shared memory. Bound
-// by memory: 8192 x 8192 bf16 in 80 us with the sums' adding (5.0 TB/s), the
-// join of 8192 x 4096 in 63 (5.3 TB/s). One workgroup a CU keeps the partial
-// sums at 4 % of the rows' bytes there.
+// by memory over many rows: 8192 x 8192 bf16 in 82 us with the sums' adding (4.9
+// TB/s), the join of 8192 x 4096 in 71 (4.7 TB/s). One workgroup a CU keeps the
+// partial sums at 4 % of the rows' bytes there; over a few hundred rows they are
+// most of them (512 x 4096: 13.7 us, 2.6 at a copy's rate). Narrow rows wait for
+// their many teams' sums, which the first team adds one after another (100000 x
+// 64: 25.7 us, 7.8). binary32 planes in the join spill 4 to 11 registers a lane
+// up to 4096 columns, at the copy's rate over many rows all the same (8192 x 4096:
+// 138 us, 4.9 TB/s).
 template <typename T, typename W, int L, bool JOIN>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(RowsGradArgs a) {
   constexpr int R = 1024 / L;
@@ -443,7 +448,11 @@ struct NormGradWide {
 };
 
 // The gradient in front of an activation, and its column sums from before
-// the rounding.
+// the rounding. It is rounded to the operands' type because the matrix cores
+// take no wider one beside them: dx and dw are 2.3e-3 from the 64-bit result in
+// bf16 where a gradient in 32 bits would leave 1.7e-3, their own rounding; two
+// terms of the type would hold it, at twice the products' time (220 to 240 us of
+// 8192 x 4096 x 2048).
 template <typename T, int ACT, bool BIAS>
 struct ActGrad {
   static constexpr int SUMS = BIAS ? 1 : 0, UNROLL = 4;
@@ -510,7 +519,8 @@ uint32_t row_groups(uint32_t teams) { return teams < kMaxGroups ? teams : kMaxGr
 // Workgroups of the backward norm kernel: one a CU.
 constexpr uint32_t kGradGroups = 256;
 // Widest row whose sums stay in registers, one group a lane. Two groups spill:
-// 2048 x 16384 bf16 took 243 us, and takes 79 in two kernels.
+// 2048 x 16384 bf16 took 243 us, and takes 71 in two kernels, which read dy and x
+// twice (41 at a copy's rate).
 constexpr uint32_t kGradCols = 8192;
 
 hipError_t launch_column_sum(const ColumnSumArgs& a, hipStream_t stream) {
